@@ -394,6 +394,137 @@ XSYMV_API const char *xgemv_variant_name(char type, int index);
 XSYMV_API int xgemv_set_variant(char type, int index);
 XSYMV_API int xgemv_selected_variant(char type);
 
+/* ---- a linear layer in 8 bits -------------------------------------------
+ * The report has no counterpart to these entry points.  A model's weight is
+ * the same kind of operand as the matrix of a SYMV: it stays in HBM and
+ * meets one vector at a time (a token), so the product is bound by its bytes
+ * and 8-bit integers with scales make them a half or a quarter.  The calls
+ * are the way from the residual stream to the layer's output, and what
+ * training needs of it:
+ *
+ *   x<quant>     a matrix to 8 bits with a scale for each column (weights:
+ *                one column per output channel; activations: one per token)
+ *   x<dequant>   the values that 8-bit elements stand for
+ *   x<rmsquant>  residual addition, root-mean-square norm, 8-bit output
+ *   x<rmsgrad>   the gradient of that norm and addition, the rounding to 8
+ *                bits taken as the identity
+ *   x<gemmq>     the product of two 8-bit matrices with their scales
+ *
+ * Suffix: the type T of everything that is neither 8 bits nor a scale:
+ * _s float, _h IEEE half, _b bfloat16.  Scales, reciprocal norms and the
+ * gradient of the norm's weight are float whatever T is.
+ *
+ * Conventions: column-major, as everywhere in this header; a column is one
+ * token (or one output channel) and its elements are contiguous.  m is the
+ * length of a column and n the number of columns; element (i, j) of X is
+ * X[i + j*ldx], with ldx >= max(1, m), and offsets are computed in 64 bits.
+ * All pointers are DEVICE pointers aligned to their element, owned by the
+ * caller; any alignment beyond that and any leading dimension work (rows of
+ * 16-byte aligned columns are faster).  Only the m elements of each column
+ * are read or written, never the padding between columns.  Arrays written
+ * must not overlap other arguments, except where "in place" is said: then
+ * pointer and leading dimension must both be the same.  m = 0 or n = 0
+ * returns at once (x<rmsgrad> with n = 0 sets dG to 0 first).
+ *
+ * Work is enqueued on the library's stream and runs asynchronously, like
+ * the SYMV calls; x<rmsgrad> and x<gemmq> keep partial results in library
+ * workspaces per (device, stream), grown on demand.  Results are
+ * bit-identical from run to run.  Every sum, norm and scale is formed in 32
+ * bits or more, and a result is rounded to T once.
+ *
+ * Status: 0; the position of the first bad argument in its signature (a
+ * negative size, a leading dimension below max(1, rows), eps negative or
+ * NaN), with nothing enqueued; XSYMV_ERR_VALUE for a NULL pointer that is not
+ * optional; or XSYMV_ERR_*. */
+typedef struct { unsigned short bits; } xsymv_f16;    /* IEEE half     */
+typedef struct { unsigned short bits; } xsymv_bf16;   /* bfloat16      */
+
+/* scale[j] = max_i |X(i,j)| / 127,  Q(i,j) = X(i,j) / scale[j] rounded to the
+ * nearest integer, ties to even (-127 .. 127).  A column of zeros (or one
+ * so small that its scale rounds to zero) has scale 0 and Q 0.  A column
+ * that holds an infinity or a NaN has scale NaN and Q 0, so that everything
+ * computed from it is NaN.
+ * Bad arguments: 1 m, 2 n, 4 ldx, 6 ldq. */
+XSYMV_API int xquant_s(int m, int n, const float *X, int ldx, signed char *Q, int ldq,
+                       float *scale);
+XSYMV_API int xquant_h(int m, int n, const xsymv_f16 *X, int ldx, signed char *Q, int ldq,
+                       float *scale);
+XSYMV_API int xquant_b(int m, int n, const xsymv_bf16 *X, int ldx, signed char *Q, int ldq,
+                       float *scale);
+
+/* X(i,j) = Q(i,j) * scale[j].  T need not be the type that was quantised.
+ * Bad arguments: 1 m, 2 n, 4 ldq, 7 ldx. */
+XSYMV_API int xdequant_s(int m, int n, const signed char *Q, int ldq, const float *scale,
+                         float *X, int ldx);
+XSYMV_API int xdequant_h(int m, int n, const signed char *Q, int ldq, const float *scale,
+                         xsymv_f16 *X, int ldx);
+XSYMV_API int xdequant_b(int m, int n, const signed char *Q, int ldq, const float *scale,
+                         xsymv_bf16 *X, int ldx);
+
+/* For each column j:
+ *   H(i,j)  = X(i,j) + R(i,j), rounded to T (the new residual)
+ *   rstd[j] = 1 / sqrt(mean_i H(i,j)^2 + eps)
+ *   Q, scale = x<quant> of H(i,j) * rstd[j] * G[i]
+ * The norm is that of the rounded H, so that x<rmsgrad>, which is given H, is
+ * its gradient.
+ * R     NULL: H = X (ldr is not used).
+ * G     NULL: all ones.
+ * H     NULL: not stored (ldh is not used).  In place: H may be X or R.
+ * rstd  NULL: not stored.
+ * Squares that overflow or underflow float are summed scaled: any finite H
+ * has the norm of its definition.
+ * Bad arguments: 1 m, 2 n, 4 ldx, 6 ldr, 8 eps, 10 ldh, 12 ldq. */
+XSYMV_API int xrmsquant_s(int m, int n, const float *X, int ldx, const float *R, int ldr,
+                          const float *G, float eps, float *H, int ldh, signed char *Q, int ldq,
+                          float *scale, float *rstd);
+XSYMV_API int xrmsquant_h(int m, int n, const xsymv_f16 *X, int ldx, const xsymv_f16 *R, int ldr,
+                          const xsymv_f16 *G, float eps, xsymv_f16 *H, int ldh, signed char *Q,
+                          int ldq, float *scale, float *rstd);
+XSYMV_API int xrmsquant_b(int m, int n, const xsymv_bf16 *X, int ldx, const xsymv_bf16 *R,
+                          int ldr, const xsymv_bf16 *G, float eps, xsymv_bf16 *H, int ldh,
+                          signed char *Q, int ldq, float *scale, float *rstd);
+
+/* The gradient of the addition and the norm.  dY is the gradient with respect
+ * to the norm's output H*rstd*G (through the 8-bit rounding as through the
+ * identity), dR the gradient that reaches H directly (the residual path).
+ * With u(i) = H(i,j) rstd[j] and a(i) = dY(i,j) G[i]:
+ *   dX(i,j) = dR(i,j) + rstd[j] * (a(i) - u(i) * mean_i(a(i) u(i)))
+ *   dG[i]   = sum_j dY(i,j) u(i)
+ * dX is the gradient with respect to X and to R alike.
+ * G     NULL: all ones.   dR  NULL: zero (lddr is not used).
+ * dG    NULL: not computed.
+ * In place: dX may be dY, dR or H.
+ * Bad arguments: 1 m, 2 n, 4 lddy, 6 ldh, 10 lddr, 12 lddx. */
+XSYMV_API int xrmsgrad_s(int m, int n, const float *dY, int lddy, const float *H, int ldh,
+                         const float *G, const float *rstd, const float *dR, int lddr, float *dX,
+                         int lddx, float *dG);
+XSYMV_API int xrmsgrad_h(int m, int n, const xsymv_f16 *dY, int lddy, const xsymv_f16 *H, int ldh,
+                         const xsymv_f16 *G, const float *rstd, const xsymv_f16 *dR, int lddr,
+                         xsymv_f16 *dX, int lddx, float *dG);
+XSYMV_API int xrmsgrad_b(int m, int n, const xsymv_bf16 *dY, int lddy, const xsymv_bf16 *H,
+                         int ldh, const xsymv_bf16 *G, const float *rstd, const xsymv_bf16 *dR,
+                         int lddr, xsymv_bf16 *dX, int lddx, float *dG);
+
+/* Y := alpha * diag(sw) * W^T * X * diag(sx) + beta * Y:
+ *   Y(i,j) = alpha * sw[i] * sx[j] * sum_p W(p,i) X(p,j) + beta * Y(i,j)
+ * W is k-by-m (column i: output channel i), X k-by-n (column j: token j),
+ * both signed 8-bit (-128 .. 127), Y m-by-n of type T.
+ * sw, sx  NULL: all ones.
+ * beta = 0: Y is written without being read.  alpha = 0 or k = 0: W, X and
+ * the scales are not read; if then beta = 1, nothing is touched.
+ * The sum of integer products is exact up to 2^24 in size (always, for
+ * k <= 1040) and accumulated in float or int32 beyond.
+ * Bad arguments: 1 m, 2 n, 3 k, 6 ldw, 9 ldx, 13 ldy. */
+XSYMV_API int xgemmq_s(int m, int n, int k, float alpha, const signed char *W, int ldw,
+                       const float *sw, const signed char *X, int ldx, const float *sx,
+                       float beta, float *Y, int ldy);
+XSYMV_API int xgemmq_h(int m, int n, int k, float alpha, const signed char *W, int ldw,
+                       const float *sw, const signed char *X, int ldx, const float *sx,
+                       float beta, xsymv_f16 *Y, int ldy);
+XSYMV_API int xgemmq_b(int m, int n, int k, float alpha, const signed char *W, int ldw,
+                       const float *sw, const signed char *X, int ldx, const float *sx,
+                       float beta, xsymv_bf16 *Y, int ldy);
+
 #ifdef __cplusplus
 }
 #endif

@@ -36,6 +36,10 @@ __all__ = [
     "ELEM_BYTES_BY_KIND", "SHARD_ENTRY_POINTS", "REDUCE_ENTRY_POINTS", "symv_shard", "symv_reduce", "xsymv_shard_bounds",
     "xsymv_s_shard", "xsymv_d_shard", "xhemv_c_shard", "xhemv_z_shard", "xsymv_w_shard",
     "xsymv_s_reduce", "xsymv_d_reduce", "xhemv_c_reduce", "xhemv_z_reduce", "xsymv_w_reduce",
+    "quant", "dequant", "rmsquant", "rmsgrad", "gemmq",
+    "xquant_s", "xquant_h", "xquant_b", "xdequant_s", "xdequant_h", "xdequant_b",
+    "xrmsquant_s", "xrmsquant_h", "xrmsquant_b", "xrmsgrad_s", "xrmsgrad_h", "xrmsgrad_b",
+    "xgemmq_s", "xgemmq_h", "xgemmq_b",
 ]
 
 ENTRY_POINTS = {"s": "xsymv_s", "d": "xsymv_d", "c": "xhemv_c", "z": "xhemv_z", "w": "xsymv_w"}
@@ -137,6 +141,20 @@ def load():
             fn = getattr(lib, "xgemv_" + k)
             fn.argtypes = [c_int, scal[k], vp, c_int, vp, c_int, scal[k], vp, c_int]
             fn.restype = c_int
+        flt = ctypes.c_float
+        for k in "shb":
+            for name, args in (
+                    ("xquant_", [c_int, c_int, vp, c_int, vp, c_int, vp]),
+                    ("xdequant_", [c_int, c_int, vp, c_int, vp, vp, c_int]),
+                    ("xrmsquant_", [c_int, c_int, vp, c_int, vp, c_int, vp, flt, vp, c_int, vp,
+                                    c_int, vp, vp]),
+                    ("xrmsgrad_", [c_int, c_int, vp, c_int, vp, c_int, vp, vp, vp, c_int, vp,
+                                   c_int, vp]),
+                    ("xgemmq_", [c_int, c_int, c_int, flt, vp, c_int, vp, vp, c_int, vp, flt, vp,
+                                 c_int])):
+                fn = getattr(lib, name + k)
+                fn.argtypes = args
+                fn.restype = c_int
         lib.xgemv_variant_count.argtypes = [c_char]
         lib.xgemv_variant_count.restype = c_int
         lib.xgemv_variant_name.argtypes = [c_char, c_int]
@@ -486,3 +504,68 @@ def xgemv_set_variant(kind: str, index: int) -> int:
 
 def xgemv_selected_variant(kind: str) -> int:
     return load().xgemv_selected_variant(kind.encode())
+
+
+# ------------------------------------------- a linear layer in 8 bits -----
+
+def _q8_call(name, kind, stream):
+    """The entry point of `name` for kind ('s' float, 'h' half, 'b' bfloat16),
+    with the stream set."""
+    if kind not in ("s", "h", "b"):
+        raise ValueError("kind must be 's', 'h' or 'b'")
+    lib = _lib if _lib is not None else load()
+    _use_stream(lib, stream)
+    return getattr(lib, name + kind)
+
+
+def quant(kind, m, n, X, ldx, Q, ldq, scale, stream=None) -> int:
+    """The n columns of m elements of X to 8 bits (Q) with a scale each:
+    scale[j] = max|X(:,j)| / 127, Q = X / scale rounded to nearest even."""
+    return _q8_call("xquant_", kind, stream)(m, n, _ptr(X), ldx, _ptr(Q), ldq, _ptr(scale))
+
+
+def dequant(kind, m, n, Q, ldq, scale, X, ldx, stream=None) -> int:
+    """X(i,j) = Q(i,j) * scale[j], rounded to kind."""
+    return _q8_call("xdequant_", kind, stream)(m, n, _ptr(Q), ldq, _ptr(scale), _ptr(X), ldx)
+
+
+def rmsquant(kind, m, n, X, ldx, R, ldr, G, eps, H, ldh, Q, ldq, scale, rstd,
+             stream=None) -> int:
+    """H = X + R (R may be None), its root-mean-square norm over each column
+    times G (None: ones), quantised to Q and scale.  H and rstd may be None;
+    H may be X or R."""
+    return _q8_call("xrmsquant_", kind, stream)(
+        m, n, _ptr(X), ldx, _ptr(R), ldr, _ptr(G), eps, _ptr(H), ldh, _ptr(Q), ldq, _ptr(scale),
+        _ptr(rstd))
+
+
+def rmsgrad(kind, m, n, dY, lddy, H, ldh, G, rstd, dR, lddr, dX, lddx, dG, stream=None) -> int:
+    """The gradient of rmsquant, straight through the rounding: dX (with
+    respect to X and R alike) from dY (the norm's output) and dR (H itself,
+    may be None), and dG (float, may be None), from the H and rstd that
+    rmsquant stored."""
+    return _q8_call("xrmsgrad_", kind, stream)(
+        m, n, _ptr(dY), lddy, _ptr(H), ldh, _ptr(G), _ptr(rstd), _ptr(dR), lddr, _ptr(dX), lddx,
+        _ptr(dG))
+
+
+def gemmq(kind, m, n, k, alpha, W, ldw, sw, X, ldx, sx, beta, Y, ldy, stream=None) -> int:
+    """Y := alpha * diag(sw) W^T X diag(sx) + beta * Y with W (k by m) and X
+    (k by n) of 8-bit integers, sw and sx float (None: ones), Y of kind."""
+    return _q8_call("xgemmq_", kind, stream)(
+        m, n, k, alpha, _ptr(W), ldw, _ptr(sw), _ptr(X), ldx, _ptr(sx), beta, _ptr(Y), ldy)
+
+
+def _q8_fn(generic, kind):
+    def f(*args, **kwargs):
+        return generic(kind, *args, **kwargs)
+    f.__name__ = "x%s_%s" % (generic.__name__, kind)
+    f.__doc__ = "``%s`` for kind '%s'." % (generic.__name__, kind)
+    return f
+
+
+xquant_s, xquant_h, xquant_b = (_q8_fn(quant, k) for k in "shb")
+xdequant_s, xdequant_h, xdequant_b = (_q8_fn(dequant, k) for k in "shb")
+xrmsquant_s, xrmsquant_h, xrmsquant_b = (_q8_fn(rmsquant, k) for k in "shb")
+xrmsgrad_s, xrmsgrad_h, xrmsgrad_b = (_q8_fn(rmsgrad, k) for k in "shb")
+xgemmq_s, xgemmq_h, xgemmq_b = (_q8_fn(gemmq, k) for k in "shb")

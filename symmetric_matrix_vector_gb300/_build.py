@@ -19,7 +19,7 @@ LIBNAME = "libxsymv.so"
 LIBPATH = os.path.join(LIBDIR, LIBNAME)
 
 UNITS = ["xsymv_api", "xsymv_probe", "xsymv_s", "xsymv_d", "xsymv_c", "xsymv_z", "xsymv_w",
-         "xsymv_gemv"]
+         "xsymv_gemv", "xsymv_q8_rows", "xsymv_q8_gemm"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-fvisibility=hidden",
                      "-I", INCLUDE]

@@ -465,11 +465,19 @@ XSYMV_API void* xsymv_get_stream(void) { return reinterpret_cast<void*>(g_stream
 XSYMV_API const char* xsymv_status_string(int status) {
   switch (status) {
     case 0: return "success";
-    case 1: return "invalid argument 1 (uplo): must be 'U', 'u', 'L' or 'l'";
-    case 2: return "invalid argument 2 (n): must be >= 0";
-    case 5: return "invalid argument 5 (lda): must be >= max(1, n)";
-    case 7: return "invalid argument 7 (incx): must be non-zero";
-    case 10: return "invalid argument 10 (incy): must be non-zero";
+    // positions of the SYMV signature; other signatures have other arguments there
+    case 1: return "invalid argument 1 (in a SYMV call uplo: must be 'U', 'u', 'L' or 'l')";
+    case 2: return "invalid argument 2 (in a SYMV call n: must be >= 0)";
+    case 3: return "invalid argument 3";
+    case 4: return "invalid argument 4";
+    case 5: return "invalid argument 5 (in a SYMV call lda: must be >= max(1, n))";
+    case 6: return "invalid argument 6";
+    case 7: return "invalid argument 7 (in a SYMV call incx: must be non-zero)";
+    case 8: return "invalid argument 8";
+    case 9: return "invalid argument 9";
+    case 10: return "invalid argument 10 (in a SYMV call incy: must be non-zero)";
+    case 12: return "invalid argument 12";
+    case 13: return "invalid argument 13";
     case XSYMV_ERR_CUDA: return "a CUDA call or kernel launch failed";
     case XSYMV_ERR_ALLOC: return "workspace allocation failed";
     case XSYMV_ERR_DEVICE: return "no usable device (compute capability 10.3 required)";

@@ -1,0 +1,207 @@
+"""GPU parity of the product of 8-bit matrices (x<gemmq>) against a 64-bit
+product: from one token to prompts, odd sizes, depths of zero and one, padded
+and unaligned columns, every type, alpha and beta, missing scales, the largest
+integers, NaN scales, offsets beyond 32 bits."""
+import pytest
+import torch
+
+import symmetric_matrix_vector_gb300 as xs
+from tests import q8_reference as ref
+from tests.q8_reference import DTYPES, UNIT, Matrix
+
+pytestmark = pytest.mark.gpu
+
+LAYOUTS = [(0, 0), (16, 0), (1, 0), (3, 1), (16, 16), (0, 5)]
+TOKENS = [1, 2, 3, 5, 8, 9, 16, 17, 31, 33, 64, 65, 100, 127, 129, 256, 257, 300, 513]
+
+
+def gen(seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return g
+
+
+def integers(g, n, k, lo=-127, hi=127):
+    return torch.randint(lo, hi + 1, (n, k), generator=g, device="cuda", dtype=torch.int32).to(torch.int8)
+
+
+def check(kind, m, n, k, g, pad=0, off=0, alpha=1.0, beta=0.0, scales=True, w=None, x=None):
+    dt = DTYPES[kind]
+    W = Matrix(m, max(k, 1), torch.int8, max(k, 1) + pad, off,
+               integers(g, m, max(k, 1)) if w is None else w)
+    X = Matrix(n, max(k, 1), torch.int8, max(k, 1) + pad, off,
+               integers(g, n, max(k, 1)) if x is None else x)
+    sw = torch.rand((m,), generator=g, device="cuda") * 1e-3 + 1e-5
+    sx = torch.rand((n,), generator=g, device="cuda") * 1e-2 + 1e-4
+    y0 = torch.randn((n, m), generator=g, device="cuda").to(dt)
+    # beta = 0 must not read Y
+    Y = Matrix(n, m, dt, m + pad, off, y0 if beta != 0 else torch.full_like(y0, float("nan")))
+    assert xs.gemmq(kind, m, n, k, alpha, W.ptr, W.ld, sw if scales else None, X.ptr, X.ld,
+                    sx if scales else None, beta, Y.ptr, Y.ld) == 0
+    torch.cuda.synchronize()
+    if not scales:
+        sw, sx = torch.ones_like(sw), torch.ones_like(sx)
+    y64, size = ref.gemmq(W.rows[:, :k], X.rows[:, :k], alpha, sw, sx, beta, y0)
+    bound = UNIT[kind] * y64.abs() + (1 + UNIT[kind]) * size + (2.0 ** -25 if kind == "h" else 0)
+    bad = ~((Y.rows.double() - y64).abs() <= bound)
+    if kind == "h":     # beyond half's range
+        bad &= ~(torch.isinf(Y.rows) & (y64.abs() > 65000))
+    assert not bool(bad.any()), (kind, m, n, k, pad, off, int(bad.sum()))
+    assert Y.outside_untouched()
+
+
+@pytest.mark.parametrize("n", TOKENS)
+def test_token_counts(n):
+    g = gen(n)
+    for kind, m, k in (("b", 256, 512), ("s", 129, 1000), ("h", 100, 64), ("s", 384, 2048)):
+        for pad, off in ((0, 0), (1, 0)):
+            check(kind, m, n, k, g, pad, off)
+
+
+@pytest.mark.parametrize("k", [1, 2, 15, 16, 31, 32, 33, 63, 64, 65, 100, 127, 128, 130, 255, 256,
+                               1000, 1543, 4096, 5000, 16384])
+def test_depths(k):
+    g = gen(k)
+    for n, m in ((1, 130), (4, 64), (20, 257), (70, 128), (300, 200)):
+        check("s", m, n, k, g)
+        check("b", m, n, k, g, pad=16)
+
+
+@pytest.mark.parametrize("m", [1, 2, 7, 8, 15, 16, 63, 64, 100, 127, 128, 129, 255, 257, 500, 1000,
+                               2111, 4096, 33000])
+def test_channel_counts(m):
+    g = gen(m)
+    for n, k in ((1, 256), (3, 100), (16, 512), (50, 128), (260, 192)):
+        check("s", m, n, k, g)
+        check("h", m, n, k, g, pad=1)
+
+
+@pytest.mark.parametrize("pad,off", LAYOUTS)
+@pytest.mark.parametrize("kind", ["s", "h", "b"])
+def test_layouts_and_scalars(kind, pad, off):
+    g = gen(7 * pad + off)
+    for n in (1, 6, 24, 90, 270):
+        for alpha, beta in ((1.0, 0.0), (-0.75, 1.0), (0.5, -2.0)):
+            check(kind, 200, n, 320, g, pad, off, alpha, beta)
+        check(kind, 200, n, 320, g, pad, off, 1e-4, 0.0, scales=False)
+
+
+@pytest.mark.parametrize("n", [1, 4, 20, 80, 300])
+def test_raw_integers_are_exact(n):
+    """no scales, float output: the integer sums themselves, equal to the last bit
+    while they are below 2^24"""
+    g = gen(n)
+    for k in (64, 777, 1024):
+        w, x = integers(g, 150, k, -128, 127), integers(g, n, k, -128, 127)
+        y = torch.empty((n, 150), device="cuda")
+        assert xs.gemmq("s", 150, n, k, 1.0, w, k, None, x, k, None, 0.0, y, 150) == 0
+        torch.cuda.synchronize()
+        assert torch.equal(y.double(), x.double() @ w.double().T)
+
+
+@pytest.mark.parametrize("n", [1, 4, 20, 80, 300])
+def test_largest_integers(n):
+    """every product at its largest, of one sign: sums beyond 2^24"""
+    m, k = 140, 8192
+    for a, b in ((-128, -128), (-128, 127), (127, 127)):
+        w = torch.full((m, k), a, dtype=torch.int8, device="cuda")
+        x = torch.full((n, k), b, dtype=torch.int8, device="cuda")
+        check("s", m, n, k, gen(n), w=w, x=x)
+
+
+@pytest.mark.parametrize("n", [1, 4, 20, 80, 300])
+def test_nan_scales_stay_in_their_row_and_column(n):
+    m, k = 150, 256
+    g = gen(n)
+    w, x = integers(g, m, k), integers(g, n, k)
+    sw, sx = torch.ones((m,), device="cuda"), torch.ones((n,), device="cuda")
+    sw[149] = float("nan")
+    sx[n - 1] = float("nan")
+    y = torch.zeros((n, m), device="cuda")
+    assert xs.gemmq("s", m, n, k, 1.0, w, k, sw, x, k, sx, 0.0, y, m) == 0
+    torch.cuda.synchronize()
+    want = torch.zeros((n, m), dtype=torch.bool, device="cuda")
+    want[:, 149] = True
+    want[n - 1, :] = True
+    assert torch.equal(torch.isnan(y), want)
+
+
+@pytest.mark.parametrize("kind", ["s", "h", "b"])
+@pytest.mark.parametrize("n", [1, 20, 200])
+def test_no_product(kind, n):
+    """alpha = 0 or k = 0: Y := beta * Y, nothing else read"""
+    m, dt = 130, DTYPES[kind]
+    y0 = torch.randn((n, m), generator=gen(n), device="cuda").to(dt)
+    for alpha, k in ((0.0, 64), (1.0, 0)):
+        for beta in (0.0, 0.5, 1.0):
+            y = y0.clone() if beta != 0 else torch.full_like(y0, float("nan"))
+            assert xs.gemmq(kind, m, n, k, alpha, None, 64, None, None, 64, None, beta, y, m) == 0
+            torch.cuda.synchronize()
+            assert torch.equal(y, (y0.float() * beta).to(dt) if beta != 0 else torch.zeros_like(y0))
+
+
+@pytest.mark.parametrize("n", [1, 20, 200])
+def test_repeats_bitwise_on_another_stream(n):
+    m, k = 1000, 2000
+    g = gen(n)
+    w, x = integers(g, m, k), integers(g, n, k)
+    sw, sx = torch.rand((m,), generator=g, device="cuda"), torch.rand((n,), generator=g, device="cuda")
+    torch.cuda.synchronize()
+    outs = []
+    for stream in (torch.cuda.Stream(), torch.cuda.current_stream(), torch.cuda.Stream()):
+        with torch.cuda.stream(stream):
+            for _ in range(3):
+                y = torch.empty((n, m), device="cuda")
+                assert xs.gemmq("s", m, n, k, 1.0, w, k, sw, x, k, sx, 0.0, y, m) == 0
+                outs.append(y)
+        stream.synchronize()
+    assert all(torch.equal(outs[0], y) for y in outs[1:])
+
+
+@pytest.mark.parametrize("n", [2, 40])
+def test_offsets_beyond_32_bits(n):
+    """channels, tokens and outputs so far apart that offsets pass 2^32 bytes"""
+    m, k, ld = 5, 96, (1 << 30) - 16
+    g = gen(n)
+    wf = torch.empty(((m - 1) * ld + k,), dtype=torch.int8, device="cuda")     # 4.3 GB
+    w = wf.as_strided((m, k), (ld, 1))
+    w.copy_(integers(g, m, k))
+    ldx = (1 << 32) // n // 16 * 16 + 16 if n > 2 else (1 << 31) - 16
+    xf = torch.empty(((n - 1) * ldx + k,), dtype=torch.int8, device="cuda")
+    x = xf.as_strided((n, k), (ldx, 1))
+    x.copy_(integers(g, n, k))
+    yf = torch.empty(((n - 1) * ldx + m,), dtype=torch.bfloat16, device="cuda")
+    assert xs.gemmq("b", m, n, k, 1.0, wf, ld, None, xf, ldx, None, 0.0, yf, ldx) == 0
+    torch.cuda.synchronize()
+    assert torch.equal(yf.as_strided((n, m), (ldx, 1)),
+                       (x.double() @ w.double().T).float().bfloat16())
+    del wf, w, xf, x, yf
+    torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("kind", ["h", "b"])
+def test_norm_feeds_product(kind):
+    """rmsquant's output is the product's input as it stands: the layer against
+    the same layer in 64 bits on the 8-bit values"""
+    dt = DTYPES[kind]
+    m, k = 300, 520
+    for n in (1, 33):
+        g = gen(n)
+        x, r = (torch.randn((n, k), generator=g, device="cuda").to(dt) for _ in range(2))
+        wt = (torch.randn((m, k), generator=g, device="cuda") * 0.05).to(dt)
+        w, q = (torch.empty((c, k), dtype=torch.int8, device="cuda") for c in (m, n))
+        sw, sq = torch.empty((m,), device="cuda"), torch.empty((n,), device="cuda")
+        h, y = torch.empty_like(x), torch.empty((n, m), dtype=dt, device="cuda")
+        assert xs.quant(kind, k, m, wt, k, w, k, sw) == 0
+        assert xs.rmsquant(kind, k, n, x, k, r, k, None, 1e-5, h, k, q, k, sq, None) == 0
+        assert xs.gemmq(kind, m, n, k, 1.0, w, k, sw, q, k, sq, 0.0, y, m) == 0
+        torch.cuda.synchronize()
+        y64 = (q.double() * sq.double()[:, None]) @ (w.double() * sw.double()[:, None]).T
+        assert bool(((y.double() - y64).abs() <= UNIT[kind] * y64.abs() + 1e-6 * k ** 0.5).all())
+        # and near the layer of the unquantised values: two roundings of half a step
+        # per product, at most 1/254 of the largest of a column each
+        hn, _ = ref.rmsnorm(h.double(), 1.0, 1e-5)
+        full = hn @ wt.double().T
+        worst = (hn.abs().amax(1)[:, None] * wt.double().abs().sum(1)[None, :]
+                 + hn.abs().sum(1)[:, None] * wt.double().abs().amax(1)[None, :]) / 254 * 1.01
+        assert bool(((y.double() - full).abs() <= worst + UNIT[kind] * full.abs() + 1e-3).all())
