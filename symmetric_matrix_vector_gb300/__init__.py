@@ -172,6 +172,11 @@ def load():
 def _ptr(a) -> int:
     if a is None:
         return 0
+    try:                      # the usual argument: a CUDA tensor
+        if a.is_cuda:
+            return a.data_ptr()
+    except AttributeError:
+        pass
     if isinstance(a, int):
         return a
     if hasattr(a, "data_ptr"):

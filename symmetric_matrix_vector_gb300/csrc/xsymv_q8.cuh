@@ -42,66 +42,65 @@ __device__ __forceinline__ uint32_t magnitude_bits(float v) {
 }
 constexpr uint32_t kInfBits = 0x7f800000u;
 
-// How a column whose largest magnitude has the bits `top` is rounded to 8
-// bits: q = rint(v * pre * inv).  pre is 1 except for columns so small
-// that 127 / top would overflow (below 2^-60, taken 2^64 times larger).
-// |v| <= top makes |q| <= 127 without a clamp: v * inv is at most
+// How a column of largest magnitude a is rounded to 8 bits:
+// q = rint(v * pre * inv).  pre is 1 except for columns so small
+// that 127 / a would overflow (below 2^-60, taken 2^64 times larger).
+// |v| <= a makes |q| <= 127 without a clamp: v * inv is at most
 // 127 (1 + 2^-22) before it is rounded to an integer.
 struct Rounding {
   float scale, pre, inv;
 };
-__device__ __forceinline__ Rounding rounding_of(uint32_t top) {
+__device__ __forceinline__ Rounding rounding_of(float a) {
   Rounding r;
-  const float a = __uint_as_float(top);
-  if (top >= kInfBits) {   // an infinity or a NaN: reads back as NaN everywhere
+  if (magnitude_bits(a) >= kInfBits) {   // an infinity or a NaN: reads back as NaN everywhere
     r.scale = __uint_as_float(0x7fc00000u);
     r.pre = r.inv = 0.f;
     return r;
   }
   r.scale = a / 127.f;
   r.pre = a < 0x1p-60f ? 0x1p64f : 1.f;
+  // inv = 0 (a column of zeros, or one that is not finite): Q is 0
   r.inv = r.scale > 0.f ? 127.f / (a * r.pre) : 0.f;
   return r;
 }
-// inv = 0 (a column of zeros, or one that is not finite) gives 0 for every v
-__device__ __forceinline__ int round_q8(float v, const Rounding& r) {
-  return r.inv == 0.f ? 0 : __float2int_rn(v * r.pre * r.inv);
+// Every kernel of these operators may be launched while its predecessor on
+// the stream still runs (programmatic dependent launch hides the launch's
+// latency): await_predecessor comes before the first access to global memory,
+// and only then is the successor allowed to do the same.
+__device__ __forceinline__ void await_predecessor() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
-// Sum and maximum over a block of THREADS threads (a multiple of 32); every
-// thread returns the result.  The order of the additions is fixed.
-template <int THREADS>
-__device__ __forceinline__ float block_sum(float v, float* buf) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  __syncthreads();
-  if (threadIdx.x % 32 == 0) buf[threadIdx.x / 32] = v;
-  __syncthreads();
-  float s = 0.f;
-#pragma unroll
-  for (int w = 0; w < THREADS / 32; ++w) s += buf[w];
-  return s;
-}
-template <int THREADS>
-__device__ __forceinline__ uint32_t block_max(uint32_t v, float* buf) {
-  v = __reduce_max_sync(0xffffffffu, v);
-  __syncthreads();
-  if (threadIdx.x % 32 == 0) buf[threadIdx.x / 32] = __uint_as_float(v);
-  __syncthreads();
-  uint32_t s = 0;
-#pragma unroll
-  for (int w = 0; w < THREADS / 32; ++w) s = max(s, __float_as_uint(buf[w]));
-  return s;
+template <class... P, class... A>
+inline cudaError_t launch_after(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem,
+                                cudaStream_t st, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
 }
 
-// host: the status of a launch
-inline int launched(cudaError_t e, int kernels) {
+// host: the end of a call that launched `kernels` kernels, none of which
+// has a bounded wait.  Noting the call also tells a following SYMV call
+// that its predecessor is not a SYMV finaliser it could overlap with.
+inline int launched(cudaError_t e, int kernels, cudaStream_t st) {
   if (e != cudaSuccess) {
     record_cuda_error(e);
     return XSYMV_ERR_CUDA;
   }
   note_launches(kernels);
+  note_call_status(st, nullptr, 0);
   return XSYMV_OK;
 }
+
+inline bool short_ld(int ld, int rows) { return ld < (rows > 1 ? rows : 1); }
 
 }  // namespace xsymv

@@ -38,6 +38,7 @@ __device__ __forceinline__ void store_output(const GemmqArgs<T>& a, long long i,
 // 64-bit integers.
 template <class T>
 __global__ void gemmq_kernel(GemmqArgs<T> a) {
+  await_predecessor();
   const long long i = blockIdx.x * 32LL + threadIdx.x;
   for (long long j = blockIdx.y * 8LL + threadIdx.y; j < a.n; j += gridDim.y * 8LL) {
     if (i >= a.m) return;
@@ -47,8 +48,6 @@ __global__ void gemmq_kernel(GemmqArgs<T> a) {
     store_output(a, i, j, (float)acc);
   }
 }
-
-inline bool short_ld(int ld, int rows) { return ld < (rows > 1 ? rows : 1); }
 
 template <class T>
 int gemmq_entry(int m, int n, int k, float alpha, const int8_t* W, int ldw, const float* sw,
@@ -67,8 +66,8 @@ int gemmq_entry(int m, int n, int k, float alpha, const int8_t* W, int ldw, cons
   if (!current_device(&dev, &sms)) return XSYMV_ERR_DEVICE;
   const GemmqArgs<T> a{m, n, k, alpha, W, ldw, sw, X, ldx, sx, beta, Y, ldy};
   const dim3 grid((m + 31) / 32, (unsigned)min((n + 7LL) / 8, 65535LL));
-  gemmq_kernel<T><<<grid, dim3(32, 8), 0, current_stream()>>>(a);
-  return launched(cudaGetLastError(), 1);
+  cudaStream_t st = current_stream();
+  return launched(launch_after(gemmq_kernel<T>, grid, dim3(32, 8), 0, st, a), 1, st);
 }
 
 }  // namespace

@@ -1,41 +1,421 @@
 // Columns to 8 bits and back, the residual norm with 8-bit output and its
 // gradient (x<quant>, x<dequant>, x<rmsquant>, x<rmsgrad> of xsymv.h).
-// One thread block per column; all four are bound by the bytes of their
-// operands.  Multiply-adds are written out as fmaf, so that a call with an
-// optional operand left out rounds as the same call with that operand given.
+//
+// All of them are bound by the bytes of their operands, so every operand is
+// read once: a thread block takes one column and keeps it in registers
+// between the pass that forms the sum and the maximum and the pass that
+// writes (kNV packs of 8 elements a thread; columns longer than a block's
+// registers are read again, from L2).
+//
+// Any alignment runs at full width: the packs of a column are laid on the
+// 16-byte grid of the operand that is written (its first pack may begin
+// before the column, its last end after it: those elements are masked), and
+// an operand on another grid is read as the aligned pieces around the pack,
+// shifted into place.
+//
+// Multiply-adds are written out, so that a call with an optional operand left
+// out rounds as the same call with that operand given.
+#include <algorithm>
+
 #include "xsymv_q8.cuh"
 
 namespace xsymv {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kPack = 8;
+constexpr int kWarps = 32;   // of a block, at most
+constexpr int kSmemPerSm = 227 * 1024;
+constexpr int kBlockSmem = 2048;   // a block's reserve and its reduction buffers
+
+// ------------------------------------------------------ a column's elements --
+
+// a pack as 32-bit words, and as four pairs of floats
+template <class T>
+struct Raw {
+  static constexpr int N = kPack * sizeof(T) / 4;
+  uint32_t w[N];
+};
+struct Floats {
+  float2 v[kPack / 2];
+};
+__device__ __forceinline__ Floats floats_of(const Raw<float>& r) {
+  Floats f;
+#pragma unroll
+  for (int k = 0; k < kPack / 2; ++k)
+    f.v[k] = make_float2(__uint_as_float(r.w[2 * k]), __uint_as_float(r.w[2 * k + 1]));
+  return f;
+}
+__device__ __forceinline__ Floats floats_of(const Raw<__half>& r) {
+  Floats f;
+#pragma unroll
+  for (int k = 0; k < kPack / 2; ++k)
+    f.v[k] = __half22float2(*reinterpret_cast<const __half2*>(&r.w[k]));
+  return f;
+}
+__device__ __forceinline__ Floats floats_of(const Raw<__nv_bfloat16>& r) {
+  Floats f;
+#pragma unroll
+  for (int k = 0; k < kPack / 2; ++k)
+    f.v[k] = make_float2(__uint_as_float(r.w[k] << 16), __uint_as_float(r.w[k] & 0xffff0000u));
+  return f;
+}
+template <class T>
+__device__ __forceinline__ Raw<T> raw_of(const Floats& f);
+template <>
+__device__ __forceinline__ Raw<float> raw_of<float>(const Floats& f) {
+  Raw<float> r;
+#pragma unroll
+  for (int k = 0; k < kPack / 2; ++k) {
+    r.w[2 * k] = __float_as_uint(f.v[k].x);
+    r.w[2 * k + 1] = __float_as_uint(f.v[k].y);
+  }
+  return r;
+}
+template <>
+__device__ __forceinline__ Raw<__half> raw_of<__half>(const Floats& f) {
+  Raw<__half> r;
+#pragma unroll
+  for (int k = 0; k < kPack / 2; ++k) {
+    const __half2 h = __float22half2_rn(f.v[k]);
+    r.w[k] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+  return r;
+}
+template <>
+__device__ __forceinline__ Raw<__nv_bfloat16> raw_of<__nv_bfloat16>(const Floats& f) {
+  Raw<__nv_bfloat16> r;
+#pragma unroll
+  for (int k = 0; k < kPack / 2; ++k) {
+    const __nv_bfloat162 h = __float22bfloat162_rn(f.v[k]);
+    r.w[k] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+  return r;
+}
+
+// bytes of the aligned pieces that packs of T are loaded and stored by
+template <class T>
+constexpr int kPiece = sizeof(T) == 1 ? 8 : 16;
+
+// elements between the 16-byte boundary (8-byte, of 8-bit elements) and `row`
+template <bool GRID, class T>
+__device__ __forceinline__ int head_of(const T* row) {
+  return GRID ? 0 : (int)(reinterpret_cast<uintptr_t>(row) % kPiece<T>) / (int)sizeof(T);
+}
+// first element of this thread's pack p; may lie before the column
+__device__ __forceinline__ int first_of(int p, int head) {
+  return (p * (int)blockDim.x + (int)threadIdx.x) * kPack - head;
+}
 
 template <class T>
-__global__ void quant_kernel(int m, const T* X, long long ldx, int8_t* Q, long long ldq,
-                             float* scale) {
-  __shared__ float buf[32];
-  const long long j = blockIdx.x;
+__device__ __forceinline__ void load_piece(uint32_t* w, uintptr_t at) {
+  if (kPiece<T> == 16) {
+    const uint4 v = *reinterpret_cast<const uint4*>(at);
+    w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+  } else {
+    const uint2 v = *reinterpret_cast<const uint2*>(at);
+    w[0] = v.x, w[1] = v.y;
+  }
+}
+
+// w[0 .. N] := w[off / 4 ..] of N + 4 words (off < 16), or of N + 2 (off < 8)
+template <int N, int M>
+__device__ __forceinline__ void shift_words(uint32_t (&w)[M], unsigned off) {
+  if (M == N + 4 && (off & 8))
+#pragma unroll
+    for (int k = 0; k < N + 2; ++k) w[k] = w[k + (M == N + 4 ? 2 : 0)];
+  if (off & 4)
+#pragma unroll
+    for (int k = 0; k < N + 1; ++k) w[k] = w[k + 1];
+}
+
+// elements first .. first+7 of the m of `row`, zeros outside 0 .. m-1.
+// GRID: every operand's columns start on the grid of 16-byte pieces (8-byte
+// ones of 8-bit elements) and are whole packs long, the usual case: a pack
+// is all of the column or all outside, and no element is looked at singly
+// (rmsquant 1024 x 16384 halves: 23 us without, 14 us with it).
+template <bool GRID, class T>
+__device__ __forceinline__ Raw<T> load8(const T* row, int first, int m) {
+  constexpr int N = Raw<T>::N, P = kPiece<T> / 4;
+  Raw<T> r;
+  if (GRID) {
+#pragma unroll
+    for (int k = 0; k < N; ++k) r.w[k] = 0;
+    if (first < m)
+#pragma unroll
+      for (int k = 0; k < N; k += P)
+        load_piece<T>(r.w + k, reinterpret_cast<uintptr_t>(row + first) + 4 * k);
+  } else if (first >= 0 && first + kPack <= m) {
+    const uintptr_t at = reinterpret_cast<uintptr_t>(row + first);
+    const unsigned off = at % kPiece<T>;
+    if (off == 0) {
+#pragma unroll
+      for (int k = 0; k < N; k += P) load_piece<T>(r.w + k, at + 4 * k);
+    } else {
+      // the pieces around the pack (each holds at least one of its elements)
+      uint32_t w[N + P];
+#pragma unroll
+      for (int k = 0; k < N + P; k += P) load_piece<T>(w + k, at - off + 4 * k);
+      shift_words<N>(w, off);
+#pragma unroll
+      for (int k = 0; k < N; ++k)
+        r.w[k] = sizeof(T) == 4 ? w[k] : __funnelshift_r(w[k], w[k + 1], (off & 3) * 8);
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < N; ++k) r.w[k] = 0;
+#pragma unroll
+    for (int e = 0; e < kPack; ++e)
+      if (first + e >= 0 && first + e < m) {
+        uint32_t b;
+        if (sizeof(T) == 4)
+          b = *reinterpret_cast<const uint32_t*>(row + first + e);
+        else if (sizeof(T) == 2)
+          b = *reinterpret_cast<const uint16_t*>(row + first + e);
+        else
+          b = *reinterpret_cast<const uint8_t*>(row + first + e);
+        r.w[e * sizeof(T) / 4] |= b << (e * sizeof(T) % 4 * 8);
+      }
+  }
+  return r;
+}
+
+// elements first .. first+7 of `row`, those within 0 .. m-1
+template <bool GRID, class T>
+__device__ __forceinline__ void store8(T* row, int first, int m, const Raw<T>& r) {
+  constexpr int N = Raw<T>::N, P = kPiece<T> / 4;
+  const uintptr_t at = reinterpret_cast<uintptr_t>(row) + (long long)first * (int)sizeof(T);
+  if (GRID ? first < m : first >= 0 && first + kPack <= m && at % kPiece<T> == 0) {
+#pragma unroll
+    for (int k = 0; k < N; k += P) {
+      if (P == 4)
+        *reinterpret_cast<uint4*>(at + 4 * k) =
+            make_uint4(r.w[k], r.w[k + 1], r.w[(k + 2) % N], r.w[(k + 3) % N]);
+      else
+        *reinterpret_cast<uint2*>(at + 4 * k) = make_uint2(r.w[k], r.w[k + 1]);
+    }
+  } else if (!GRID) {
+#pragma unroll
+    for (int e = 0; e < kPack; ++e)
+      if (first + e >= 0 && first + e < m) {
+        const uint32_t b = r.w[e * sizeof(T) / 4] >> (e * sizeof(T) % 4 * 8);
+        if (sizeof(T) == 4)
+          *reinterpret_cast<uint32_t*>(row + first + e) = b;
+        else if (sizeof(T) == 2)
+          *reinterpret_cast<uint16_t*>(row + first + e) = (uint16_t)b;
+        else
+          *reinterpret_cast<uint8_t*>(row + first + e) = (uint8_t)b;
+      }
+  }
+}
+
+// store8 of a warp's 32 packs in a row, all lanes at once.  Off the 16-byte
+// grid every lane writes the aligned pieces that begin in the previous
+// lane's pack; the warp's first and last pieces, shared with other warps, are
+// written element by element.
+template <bool GRID, class T>
+__device__ __forceinline__ void store_warp(T* row, int first, int m, const Raw<T>& r) {
+  constexpr int N = Raw<T>::N;
+  if (GRID) {
+    store8<true>(row, first, m, r);
+    return;
+  }
+  const uintptr_t at = reinterpret_cast<uintptr_t>(row) + (long long)first * (int)sizeof(T);
+  const unsigned off = at % 16;
+  if (off == 0 || !__all_sync(0xffffffffu, first + kPack <= m)) {
+    store8<false>(row, first, m, r);
+    return;
+  }
+  // this lane's pieces are the N words from byte 16 - off of
+  // (the previous lane's last 16 bytes, this lane's pack)
+  uint32_t w[N + 4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) w[k] = __shfl_up_sync(0xffffffffu, r.w[N - 4 + k], 1);
+#pragma unroll
+  for (int k = 0; k < N; ++k) w[4 + k] = r.w[k];
+  const unsigned skip = 16 - off;
+  shift_words<N>(w, skip);
+#pragma unroll
+  for (int k = 0; k < N; ++k)
+    w[k] = sizeof(T) == 4 ? w[k] : __funnelshift_r(w[k], w[k + 1], (skip & 3) * 8);
+  const int lane = threadIdx.x % 32, own = (int)(skip / sizeof(T));   // elements before a piece ends
+#pragma unroll
+  for (int k = 0; k < N; k += 4)
+    if (k > 0 || lane > 0)
+      *reinterpret_cast<uint4*>(at - off + 4 * k) = make_uint4(w[k], w[k + 1], w[k + 2], w[k + 3]);
+  if (lane == 0) store8<false>(row + first, 0, own, r);
+  if (lane == 31) {
+#pragma unroll
+    for (int e = 0; e < kPack; ++e)
+      if (e * (int)sizeof(T) >= kPack * (int)sizeof(T) - (int)off) {
+        const uint32_t b = r.w[e * sizeof(T) / 4] >> (e * sizeof(T) % 4 * 8);
+        if (sizeof(T) == 4)
+          *reinterpret_cast<uint32_t*>(row + first + e) = b;
+        else
+          *reinterpret_cast<uint16_t*>(row + first + e) = (uint16_t)b;
+      }
+  }
+}
+
+// the larger magnitude of |top|, |v.x| and |v.y|; a NaN wins
+__device__ __forceinline__ float larger(float top, float2 v) {
+  float d;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(top), "f"(v.x), "f"(v.y));
+  return d;
+}
+
+// Columns that `rounded` cannot take as they are: those scaled before they are
+// rounded, and those whose Q is 0 although they may hold infinities or NaN
+__device__ __forceinline__ bool unusual(const Rounding& r) { return r.pre != 1.f || r.inv == 0.f; }
+__device__ __forceinline__ void prepare(Floats& f, const Rounding& r) {
+#pragma unroll
+  for (int k = 0; k < kPack / 2; ++k)
+    f.v[k] = r.inv == 0.f ? make_float2(0.f, 0.f)
+                          : __fmul2_rn(f.v[k], make_float2(r.pre, r.pre));
+}
+// 8 values to 8 bits: v * inv + 1.5 * 2^23 rounds to the nearest integer, ties
+// to even, and leaves it in the low bits
+__device__ __forceinline__ Raw<int8_t> rounded(const Floats& f, const Rounding& r) {
+  Raw<int8_t> q;
+  float2 u[kPack / 2];
+#pragma unroll
+  for (int k = 0; k < kPack / 2; ++k)
+    u[k] = __ffma2_rn(f.v[k], make_float2(r.inv, r.inv), make_float2(0x1.8p23f, 0x1.8p23f));
+#pragma unroll
+  for (int k = 0; k < 2; ++k)
+    q.w[k] = __byte_perm(
+        __byte_perm(__float_as_uint(u[2 * k].x), __float_as_uint(u[2 * k].y), 0x40),
+        __byte_perm(__float_as_uint(u[2 * k + 1].x), __float_as_uint(u[2 * k + 1].y), 0x40),
+        0x5410);
+  return q;
+}
+
+// ------------------------------------------------------- block reductions --
+
+// The sum and the largest magnitude over the block, known to every thread,
+// in a fixed order.  buf is free again after the next barrier.
+struct SumMax {
+  float sum;
+  float top;   // a magnitude, infinity or NaN
+};
+__device__ __forceinline__ SumMax block_sum_max(SumMax v, float2* buf) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v.sum += __shfl_xor_sync(0xffffffffu, v.sum, o);
+  // bits of magnitudes are ordered as the magnitudes are, NaN above all
+  v.top = __uint_as_float(__reduce_max_sync(0xffffffffu, magnitude_bits(v.top)));
+  const int warps = blockDim.x / 32, lane = threadIdx.x % 32;
+  if (warps == 1) return v;   // a warp has the column to itself
+  if (lane == 0) buf[threadIdx.x / 32] = make_float2(v.sum, v.top);
+  __syncthreads();
+  const float2 w = lane < warps ? buf[lane] : make_float2(0.f, 0.f);
+  v.sum = w.x;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v.sum += __shfl_xor_sync(0xffffffffu, v.sum, o);
+  v.top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(w.y)));
+  return v;
+}
+
+// packs a thread: the template's where it is given, else what m elements need
+template <int KNV>
+__device__ __forceinline__ int packs_of(int m, int head) {
+  const int block = (int)blockDim.x * kPack;
+  return KNV > 0 ? KNV : (m + head + block - 1) / block;
+}
+
+// ------------------------------------------------------------------ quant --
+
+// KNV packs a thread in registers; KNV = 0: any length, read twice
+template <class T, int KNV, bool GRID>
+__global__ void __launch_bounds__(1024) quant_kernel(int m, int n, const T* X, long long ldx,
+                                                     int8_t* Q, long long ldq, float* scale) {
+  __shared__ float2 buf[kWarps];
+  await_predecessor();
+  const long long j = blockIdx.x * (long long)blockDim.y + threadIdx.y;
+  if (j >= n) return;
   X += j * ldx;
   Q += j * ldq;
-  uint32_t top = 0;
-  for (int i = threadIdx.x; i < m; i += kThreads) top = max(top, magnitude_bits(to_float(X[i])));
-  const Rounding r = rounding_of(block_max<kThreads>(top, buf));
+  const int head = head_of<GRID>(Q);
+  Raw<T> x[KNV > 0 ? KNV : 1];
+  SumMax t{0.f, 0.f};
+  if (KNV > 0) {
+#pragma unroll
+    for (int p = 0; p < KNV; ++p) x[p] = load8<GRID>(X, first_of(p, head), m);
+#pragma unroll
+    for (int p = 0; p < KNV; ++p) {
+      const Floats f = floats_of(x[p]);
+#pragma unroll
+      for (int k = 0; k < kPack / 2; ++k) t.top = larger(t.top, f.v[k]);
+    }
+  } else {
+    for (int p = 0; p < packs_of<KNV>(m, head); ++p) {
+      const Floats f = floats_of(load8<GRID>(X, first_of(p, head), m));
+#pragma unroll
+      for (int k = 0; k < kPack / 2; ++k) t.top = larger(t.top, f.v[k]);
+    }
+  }
+  const Rounding r = rounding_of(block_sum_max(t, buf).top);
   if (threadIdx.x == 0) scale[j] = r.scale;
-  for (int i = threadIdx.x; i < m; i += kThreads) Q[i] = (int8_t)round_q8(to_float(X[i]), r);
+  if (KNV > 0) {
+#pragma unroll
+    for (int p = 0; p < KNV; ++p) {
+      // kept across the barrier as loaded, not as twice the registers of floats
+#pragma unroll
+      for (int k = 0; k < Raw<T>::N; ++k) asm volatile("" : "+r"(x[p].w[k]));
+      Floats f = floats_of(x[p]);
+      if (unusual(r)) prepare(f, r);
+      store8<GRID>(Q, first_of(p, head), m, rounded(f, r));
+    }
+  } else {
+    for (int p = 0; p < packs_of<KNV>(m, head); ++p) {
+      const int first = first_of(p, head);
+      Floats f = floats_of(load8<GRID>(X, first, m));
+      if (unusual(r)) prepare(f, r);
+      store8<GRID>(Q, first, m, rounded(f, r));
+    }
+  }
 }
 
-template <class T>
-__global__ void dequant_kernel(int m, const int8_t* Q, long long ldq, const float* scale, T* X,
-                               long long ldx) {
-  const long long j = blockIdx.x;
+// ---------------------------------------------------------------- dequant --
+
+// blockDim = (x along the column, y columns), kDeep packs a thread and step
+constexpr int kDeep = 4;
+template <class T, bool GRID>
+__global__ void __launch_bounds__(256) dequant_kernel(int m, int n, const int8_t* Q, long long ldq,
+                                                      const float* scale, T* X, long long ldx) {
+  await_predecessor();
+  const long long j = blockIdx.x * (long long)blockDim.y + threadIdx.y;
+  if (j >= n) return;
   const float s = scale[j];
-  for (int i = threadIdx.x; i < m; i += kThreads)
-    X[j * ldx + i] = from_float<T>((float)Q[j * ldq + i] * s);
+  Q += j * ldq;
+  X += j * ldx;
+  const int head = head_of<GRID>(X);
+  const int packs = (m + head + kPack - 1) / kPack, step = (int)blockDim.x * kDeep;
+  for (int c = (int)blockIdx.y * step; c < packs; c += (int)gridDim.y * step) {
+    Raw<int8_t> q[kDeep];
+#pragma unroll
+    for (int p = 0; p < kDeep; ++p)
+      q[p] = load8<GRID>(Q, (c + p * (int)blockDim.x + (int)threadIdx.x) * kPack - head, m);
+#pragma unroll
+    for (int p = 0; p < kDeep; ++p) {
+      Floats f;
+#pragma unroll
+      for (int e = 0; e < kPack; ++e) {
+        const float v = (float)(int8_t)(q[p].w[e / 4] >> (e % 4 * 8)) * s;
+        if (e % 2 == 0)
+          f.v[e / 2].x = v;
+        else
+          f.v[e / 2].y = v;
+      }
+      store8<GRID>(X, (c + p * (int)blockDim.x + (int)threadIdx.x) * kPack - head, m,
+                   raw_of<T>(f));
+    }
+  }
 }
+
+// --------------------------------------------------------------- rmsquant --
 
 template <class T>
 struct RmsquantArgs {
-  int m;
+  int m, n;
   const T* X;
   long long ldx;
   const T* R;
@@ -50,56 +430,149 @@ struct RmsquantArgs {
   float* rstd;
 };
 
+// The pack's h = x + r, rounded to T, as floats
 template <class T>
-__global__ void rmsquant_kernel(RmsquantArgs<T> a) {
-  __shared__ float buf[32];
-  const long long j = blockIdx.x;
-  // h in float, as stored: H may be X or R, so it is formed once per element
-  // and pass from what that pass may read
-  const T* src = a.H != nullptr ? a.H + j * a.ldh : a.X + j * a.ldx;
-  const T* add = a.H == nullptr && a.R != nullptr ? a.R + j * a.ldr : nullptr;
-  auto h_of = [&](int i) {
-    float v = to_float(src[i]);
-    if (add != nullptr) v = to_float(from_float<T>(v + to_float(add[i])));
-    return v;
-  };
-  auto g_of = [&](int i) { return a.G != nullptr ? to_float(a.G[i]) : 1.f; };
-  float sum = 0.f;
-  uint32_t top = 0;
-  for (int i = threadIdx.x; i < a.m; i += kThreads) {
-    float v = to_float(a.X[j * a.ldx + i]);
-    if (a.R != nullptr) v += to_float(a.R[j * a.ldr + i]);
-    const T h = from_float<T>(v);
-    if (a.H != nullptr) a.H[j * a.ldh + i] = h;
-    v = to_float(h);
-    sum += v * v;
-    top = max(top, magnitude_bits(v));
+__device__ __forceinline__ Raw<T> sum_of(const Raw<T>& x, const Raw<T>& r) {
+  Floats a = floats_of(x);
+  const Floats b = floats_of(r);
+#pragma unroll
+  for (int k = 0; k < kPack / 2; ++k) a.v[k] = __fadd2_rn(a.v[k], b.v[k]);
+  return raw_of<T>(a);
+}
+// ... read again after it was stored: H may be X or R, so H is read where
+// there is one
+template <bool GRID, class T>
+__device__ __forceinline__ Raw<T> reload_h(const RmsquantArgs<T>& a, long long j, int first) {
+  if (a.H != nullptr) return load8<GRID>(a.H + j * a.ldh, first, a.m);
+  const Raw<T> x = load8<GRID>(a.X + j * a.ldx, first, a.m);
+  return a.R != nullptr ? sum_of<T>(x, load8<GRID>(a.R + j * a.ldr, first, a.m)) : x;
+}
+
+// v = h * f * g of a pack: f is a power of two (1 but for squares out of range)
+template <bool GRID, class T>
+__device__ __forceinline__ Floats weighted(SumMax& t, float2& sum, const Raw<T>& h,
+                                           const RmsquantArgs<T>& a, int first, float f) {
+  Floats v = floats_of(h);
+  if (f != 1.f)
+#pragma unroll
+    for (int k = 0; k < kPack / 2; ++k) v.v[k] = __fmul2_rn(v.v[k], make_float2(f, f));
+#pragma unroll
+  for (int k = 0; k < kPack / 2; ++k) sum = __ffma2_rn(v.v[k], v.v[k], sum);
+  if (a.G != nullptr) {
+    const Floats g = floats_of(load8<GRID>(a.G, first, a.m));
+#pragma unroll
+    for (int k = 0; k < kPack / 2; ++k) v.v[k] = __fmul2_rn(v.v[k], g.v[k]);
   }
-  sum = block_sum<kThreads>(sum, buf);
-  top = block_max<kThreads>(top, buf);
-  float rstd = 1.f / sqrtf(sum / (float)a.m + a.eps);
-  if (top > 0 && top < kInfBits && !(sum > 0x1p-80f && sum < 0x1p127f)) {
-    // squares out of float's range: scaled by the largest magnitude's power of two
-    const int e = ilogbf(__uint_as_float(top));
-    float t = 0.f;
-    for (int i = threadIdx.x; i < a.m; i += kThreads) {
-      const float v = scalbnf(h_of(i), -e);
-      t += v * v;
+#pragma unroll
+  for (int k = 0; k < kPack / 2; ++k) t.top = larger(t.top, v.v[k]);
+  return v;
+}
+
+// With v = h g, q = rint(127 v / max|v|) does not depend on the norm, and
+// scale = max|v| rstd / 127: one pass forms the sum of squares and the
+// maximum, one barrier, one pass writes.
+template <class T, int KNV, bool GRID>
+__global__ void __launch_bounds__(1024) rmsquant_kernel(RmsquantArgs<T> a) {
+  __shared__ float2 buf[2][kWarps];
+  await_predecessor();
+  const long long j = blockIdx.x * (long long)blockDim.y + threadIdx.y;
+  if (j >= a.n) return;
+  int8_t* const Q = a.Q + j * a.ldq;
+  const int head = a.H != nullptr ? head_of<GRID>(a.H + j * a.ldh) : head_of<GRID>(Q);
+  Floats v[KNV > 0 ? KNV : 1];
+  SumMax t{0.f, 0.f};
+  float2 sum = make_float2(0.f, 0.f);
+  if (KNV > 0) {
+    Raw<T> x[KNV > 0 ? KNV : 1], r[KNV > 0 ? KNV : 1];
+#pragma unroll
+    for (int p = 0; p < KNV; ++p) {
+      x[p] = load8<GRID>(a.X + j * a.ldx, first_of(p, head), a.m);
+      if (a.R != nullptr) r[p] = load8<GRID>(a.R + j * a.ldr, first_of(p, head), a.m);
     }
-    t = block_sum<kThreads>(t, buf);
-    rstd = (float)(1.0 / sqrt(scalbn((double)t / a.m, 2 * e) + (double)a.eps));
+#pragma unroll
+    for (int p = 0; p < KNV; ++p) {
+      const int first = first_of(p, head);
+      if (a.R != nullptr) x[p] = sum_of<T>(x[p], r[p]);
+      if (a.H != nullptr) store8<GRID>(a.H + j * a.ldh, first, a.m, x[p]);
+      v[p] = weighted<GRID>(t, sum, x[p], a, first, 1.f);
+    }
+  } else {
+    for (int p = 0; p < packs_of<KNV>(a.m, head); ++p) {
+      const int first = first_of(p, head);
+      Raw<T> x = load8<GRID>(a.X + j * a.ldx, first, a.m);
+      if (a.R != nullptr) x = sum_of<T>(x, load8<GRID>(a.R + j * a.ldr, first, a.m));
+      if (a.H != nullptr) store8<GRID>(a.H + j * a.ldh, first, a.m, x);
+      weighted<GRID>(t, sum, x, a, first, 1.f);
+    }
   }
-  top = 0;
-  for (int i = threadIdx.x; i < a.m; i += kThreads)
-    top = max(top, magnitude_bits(h_of(i) * rstd * g_of(i)));
-  const Rounding r = rounding_of(block_max<kThreads>(top, buf));
+  t.sum = sum.x + sum.y;
+  t = block_sum_max(t, buf[0]);
+  float f = 1.f, rstd = 1.f / sqrtf(t.sum / (float)a.m + a.eps);
+  float top_rstd = rstd;   // scale = top * top_rstd / 127
+  if (!(t.sum > 0x1p-80f && t.sum < 0x1p127f && t.top > 0x1p-100f && t.top < 0x1p127f)) {
+    // Squares or products out of float's range, a column of zeros, or one
+    // that is not finite (whole blocks take this path): once more with h
+    // scaled by the power of two of its largest magnitude
+    if (blockDim.x > 32) __syncthreads();
+    const int packs = packs_of<KNV>(a.m, head);
+    SumMax u{0.f, 0.f};
+    for (int p = 0; p < packs; ++p) {
+      const Floats h = floats_of(reload_h<GRID>(a, j, first_of(p, head)));
+#pragma unroll
+      for (int k = 0; k < kPack / 2; ++k) u.top = larger(u.top, h.v[k]);
+    }
+    u = block_sum_max(u, buf[1]);
+    if (u.top > 0.f && magnitude_bits(u.top) < kInfBits) {
+      f = scalbnf(1.f, -max(ilogbf(u.top), -120));
+      t = SumMax{0.f, 0.f};
+      sum = make_float2(0.f, 0.f);
+      if (KNV > 0) {
+#pragma unroll
+        for (int p = 0; p < KNV; ++p) {
+          const int first = first_of(p, head);
+          v[p] = weighted<GRID>(t, sum, reload_h<GRID>(a, j, first), a, first, f);
+        }
+      } else {
+        for (int p = 0; p < packs; ++p) {
+          const int first = first_of(p, head);
+          weighted<GRID>(t, sum, reload_h<GRID>(a, j, first), a, first, f);
+        }
+      }
+      t.sum = sum.x + sum.y;
+      t = block_sum_max(t, buf[0]);
+      const double d = f, r = 1.0 / sqrt((double)t.sum / a.m + (double)a.eps * d * d);
+      rstd = (float)(r * d);
+      top_rstd = (float)r;
+    }
+  }
+  Rounding r = rounding_of(t.top);
+  r.scale = t.top * top_rstd / 127.f;
+  if (magnitude_bits(t.top) >= kInfBits || !(rstd < __uint_as_float(kInfBits))) {
+    r.scale = __uint_as_float(0x7fc00000u);   // reads back as NaN everywhere
+    r.inv = 0.f;
+  }
+  if (r.scale == 0.f) r.inv = 0.f;
   if (threadIdx.x == 0) {
     a.scale[j] = r.scale;
     if (a.rstd != nullptr) a.rstd[j] = rstd;
   }
-  for (int i = threadIdx.x; i < a.m; i += kThreads)
-    a.Q[j * a.ldq + i] = (int8_t)round_q8(h_of(i) * rstd * g_of(i), r);
+  if (KNV > 0) {
+#pragma unroll
+    for (int p = 0; p < KNV; ++p) {
+      if (unusual(r)) prepare(v[p], r);
+      store8<GRID>(Q, first_of(p, head), a.m, rounded(v[p], r));
+    }
+  } else {
+    for (int p = 0; p < packs_of<KNV>(a.m, head); ++p) {
+      const int first = first_of(p, head);
+      Floats w = weighted<GRID>(t, sum, reload_h<GRID>(a, j, first), a, first, f);
+      if (unusual(r)) prepare(w, r);
+      store8<GRID>(Q, first, a.m, rounded(w, r));
+    }
+  }
 }
+
+// ---------------------------------------------------------------- rmsgrad --
 
 template <class T>
 struct RmsgradArgs {
@@ -114,46 +587,328 @@ struct RmsgradArgs {
   long long lddr;
   T* dX;
   long long lddx;
-  float* dG;
+  float* parts;      // gridDim.x partial sums of dG, m apart; NULL: none wanted
 };
 
-// dG before dX, which may overwrite dY or H: one thread per row i
-template <class T>
-__global__ void rmsgrad_weight_kernel(RmsgradArgs<T> a) {
-  const int i = blockIdx.x * kThreads + threadIdx.x;
-  if (i >= a.m) return;
-  float s = 0.f;
-  for (long long j = 0; j < a.n; ++j)
-    s = fmaf(to_float(a.dY[j * a.lddy + i]), to_float(a.H[j * a.ldh + i]) * a.rstd[j], s);
-  a.dG[i] = s;
+// A pack's aligned pieces copied to shared memory without a stop at a
+// register, and its elements from there.  `slot`: the first of the pack's
+// PIECES 16-byte pieces of this thread, `apart` bytes from the next.  Off the
+// grid a pack has one piece more.  Packs at a column's end are loaded element by
+// element and kept as if on the grid; packs beyond it are never fetched.
+template <class T, bool GRID>
+struct Slot {
+  static constexpr int N = Raw<T>::N, PIECES = N / 4 + (GRID ? 0 : 1);
+  static __device__ __forceinline__ void put(uint32_t at, uint32_t a, uint32_t b, uint32_t c,
+                                             uint32_t d) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(a), "r"(b), "r"(c),
+                 "r"(d)
+                 : "memory");
+  }
+  static __device__ __forceinline__ void clear(uint32_t slot, uint32_t apart) {
+#pragma unroll
+    for (int k = 0; k < PIECES; ++k) put(slot + k * apart, 0, 0, 0, 0);
+  }
+  static __device__ __forceinline__ unsigned off(const T* row, int first, int m) {
+    return GRID || first + kPack > m
+               ? 0
+               : (unsigned)(reinterpret_cast<uintptr_t>(row + first) % 16);
+  }
+  static __device__ __forceinline__ void fetch(uint32_t slot, uint32_t apart, const T* row,
+                                               int first, int m) {
+    if (first >= m) return;
+    if (GRID || first + kPack <= m) {
+      const unsigned o = off(row, first, m);
+      const char* at = reinterpret_cast<const char*>(row + first) - o;
+#pragma unroll
+      for (int k = 0; k < PIECES; ++k)
+        if (k < N / 4 || o != 0)
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(slot + k * apart),
+                       "l"(at + 16 * k)
+                       : "memory");
+    } else {
+      const Raw<T> r = load8<false>(row, first, m);
+#pragma unroll
+      for (int k = 0; k < N; k += 4)
+        put(slot + k / 4 * apart, r.w[k], r.w[k + 1], r.w[k + 2], r.w[k + 3]);
+    }
+  }
+  static __device__ __forceinline__ Raw<T> get(uint32_t slot, uint32_t apart, const T* row,
+                                               int first, int m) {
+    Raw<T> r;
+    uint32_t w[PIECES * 4];
+#pragma unroll
+    for (int k = 0; k < PIECES; ++k)
+      asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(w[4 * k]), "=r"(w[4 * k + 1]), "=r"(w[4 * k + 2]), "=r"(w[4 * k + 3])
+                   : "r"(slot + k * apart)
+                   : "memory");
+    const unsigned o = off(row, first, m);
+    if (!GRID) shift_words<N>(w, o);
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+      r.w[k] = GRID || sizeof(T) == 4 ? w[k] : __funnelshift_r(w[k], w[k + 1], (o & 3) * 8);
+    return r;
+  }
+};
+
+// A block takes columns j = block, block + gridDim.x, ... and sums its
+// share of dG in registers on the way; the shares are added by
+// weight_sum_kernel, in block order.  KNV packs a thread.  An element's place
+// has to be the same in every column, so the packs begin at element 0 whatever
+// the alignment.  The operands of the next stages - 1 columns are on their
+// way to shared memory meanwhile, every thread's packs to slots of its own
+// (no thread waits for another's copies).
+constexpr int kMostStages = 3;
+constexpr int kGradOperands = 3;
+// 16-byte pieces of shared memory a thread and stage
+template <class T, int KNV, bool GRID>
+constexpr int kGradSlots = kGradOperands * KNV * Slot<T, GRID>::PIECES;
+
+template <class T, int KNV, bool GRID>
+__global__ void __launch_bounds__(512) rmsgrad_kernel(RmsgradArgs<T> a, int stages) {
+  using S = Slot<T, GRID>;
+  extern __shared__ uint4 slots[];
+  __shared__ float2 buf[2][kWarps];
+  await_predecessor();
+  const uint32_t apart = blockDim.x * 16u;
+  const uint32_t mine = (uint32_t)__cvta_generic_to_shared(slots) + threadIdx.x * 16u;
+  auto slot = [&](int stage, int operand, int p) {
+    return mine + ((stage * kGradOperands + operand) * KNV + p) * S::PIECES * apart;
+  };
+  auto fetch = [&](int stage, long long j) {
+    if (j < a.n) {
+      const T* dy = a.dY + j * a.lddy;
+      const T* h = a.H + j * a.ldh;
+      const T* dr = a.dR + j * a.lddr;
+#pragma unroll
+      for (int p = 0; p < KNV; ++p) {
+        const int first = first_of(p, 0);
+        S::fetch(slot(stage, 0, p), apart, dy, first, a.m);
+        S::fetch(slot(stage, 1, p), apart, h, first, a.m);
+        if (a.dR != nullptr) S::fetch(slot(stage, 2, p), apart, dr, first, a.m);
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  // what is never fetched is zero
+  for (int s = 0; s < stages; ++s)
+#pragma unroll
+    for (int o = 0; o < kGradOperands; ++o)
+#pragma unroll
+      for (int p = 0; p < KNV; ++p)
+        if (first_of(p, 0) >= a.m || (o == 2 && a.dR == nullptr)) S::clear(slot(s, o, p), apart);
+  Raw<T> g[KNV];
+  float2 dg[KNV][kPack / 2];
+#pragma unroll
+  for (int p = 0; p < KNV; ++p) {
+    Floats one;
+#pragma unroll
+    for (int k = 0; k < kPack / 2; ++k) one.v[k] = make_float2(1.f, 1.f);
+    g[p] = a.G != nullptr ? load8<GRID>(a.G, first_of(p, 0), a.m) : raw_of<T>(one);
+#pragma unroll
+    for (int k = 0; k < kPack / 2; ++k) dg[p][k] = make_float2(0.f, 0.f);
+  }
+  for (int s = 0; s < stages - 1; ++s) fetch(s, blockIdx.x + (long long)s * gridDim.x);
+  int stage = 0, phase = 0;
+  float next_rstd = blockIdx.x < a.n ? a.rstd[blockIdx.x] : 0.f;
+  for (long long j = blockIdx.x; j < a.n; j += gridDim.x, phase ^= 1) {
+    fetch(stage == 0 ? stages - 1 : stage - 1, j + (stages - 1LL) * gridDim.x);
+    const float rstd = next_rstd;
+    if (j + gridDim.x < a.n) next_rstd = a.rstd[j + gridDim.x];
+    const float2 rstd2 = make_float2(rstd, rstd);
+    const T* dy = a.dY + j * a.lddy;
+    const T* h = a.H + j * a.ldh;
+    const T* dr = a.dR + j * a.lddr;
+    // all but the copies of the columns after this one
+    if (stages == 3)
+      asm volatile("cp.async.wait_group 2;" ::: "memory");
+    else if (stages == 2)
+      asm volatile("cp.async.wait_group 1;" ::: "memory");
+    else
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
+    float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int p = 0; p < KNV; ++p) {
+      const int first = first_of(p, 0);
+      const Floats d = floats_of(S::get(slot(stage, 0, p), apart, dy, first, a.m));
+      const Floats u = floats_of(S::get(slot(stage, 1, p), apart, h, first, a.m));
+      const Floats w = floats_of(g[p]);
+#pragma unroll
+      for (int k = 0; k < kPack / 2; ++k) {
+        const float2 x = __fmul2_rn(u.v[k], rstd2);
+        dg[p][k] = __ffma2_rn(d.v[k], x, dg[p][k]);
+        sum = __ffma2_rn(__fmul2_rn(d.v[k], w.v[k]), x, sum);
+      }
+    }
+    const float c = -block_sum_max(SumMax{sum.x + sum.y, 0.f}, buf[phase]).sum / (float)a.m;
+#pragma unroll
+    for (int p = 0; p < KNV; ++p) {
+      const int first = first_of(p, 0);
+      Floats d = floats_of(S::get(slot(stage, 0, p), apart, dy, first, a.m));
+      const Floats u = floats_of(S::get(slot(stage, 1, p), apart, h, first, a.m));
+      const Floats r = floats_of(
+          S::get(slot(stage, 2, p), apart, a.dR != nullptr ? dr : nullptr, first, a.m));
+      const Floats w = floats_of(g[p]);
+#pragma unroll
+      for (int k = 0; k < kPack / 2; ++k)
+        d.v[k] = __ffma2_rn(rstd2,
+                            __ffma2_rn(__fmul2_rn(u.v[k], rstd2), make_float2(c, c),
+                                       __fmul2_rn(d.v[k], w.v[k])),
+                            r.v[k]);
+      store_warp<GRID>(a.dX + j * a.lddx, first, a.m, raw_of<T>(d));
+    }
+    stage = stage + 1 == stages ? 0 : stage + 1;
+  }
+  if (a.parts != nullptr) {
+#pragma unroll
+    for (int p = 0; p < KNV; ++p)
+#pragma unroll
+      for (int k = 0; k < kPack / 2; ++k) {
+        const int i = first_of(p, 0) + 2 * k;
+        if (i < a.m) a.parts[(long long)blockIdx.x * a.m + i] = dg[p][k].x;
+        if (i + 1 < a.m) a.parts[(long long)blockIdx.x * a.m + i + 1] = dg[p][k].y;
+      }
+  }
 }
 
+// Columns longer than a block's registers: dX with every operand read twice
 template <class T>
-__global__ void rmsgrad_kernel(RmsgradArgs<T> a) {
-  __shared__ float buf[32];
+__global__ void __launch_bounds__(1024) rmsgrad_long_kernel(RmsgradArgs<T> a) {
+  __shared__ float2 buf[kWarps];
+  await_predecessor();
   const long long j = blockIdx.x;
   const float rstd = a.rstd[j];
-  const T* dy = a.dY + j * a.lddy;
-  const T* h = a.H + j * a.ldh;
-  float s = 0.f;
-  for (int i = threadIdx.x; i < a.m; i += kThreads) {
-    const float g = a.G != nullptr ? to_float(a.G[i]) : 1.f;
-    s = fmaf(to_float(dy[i]) * g, to_float(h[i]) * rstd, s);
+  const float2 rstd2 = make_float2(rstd, rstd);
+  T* const dx = a.dX + j * a.lddx;
+  const int head = head_of<false>(dx), packs = packs_of<0>(a.m, head);
+  // a and u of the pack
+  auto load = [&](Floats& d, Floats& u, int first) {
+    d = floats_of(load8<false>(a.dY + j * a.lddy, first, a.m));
+    u = floats_of(load8<false>(a.H + j * a.ldh, first, a.m));
+#pragma unroll
+    for (int k = 0; k < kPack / 2; ++k) u.v[k] = __fmul2_rn(u.v[k], rstd2);
+    if (a.G != nullptr) {
+      const Floats g = floats_of(load8<false>(a.G, first, a.m));
+#pragma unroll
+      for (int k = 0; k < kPack / 2; ++k) d.v[k] = __fmul2_rn(d.v[k], g.v[k]);
+    }
+  };
+  float2 sum = make_float2(0.f, 0.f);
+  for (int p = 0; p < packs; ++p) {
+    Floats d, u;
+    load(d, u, first_of(p, head));
+#pragma unroll
+    for (int k = 0; k < kPack / 2; ++k) sum = __ffma2_rn(d.v[k], u.v[k], sum);
   }
-  const float c = block_sum<kThreads>(s, buf) / (float)a.m;
-  for (int i = threadIdx.x; i < a.m; i += kThreads) {
-    const float g = a.G != nullptr ? to_float(a.G[i]) : 1.f;
-    const float d = a.dR != nullptr ? to_float(a.dR[j * a.lddr + i]) : 0.f;
-    a.dX[j * a.lddx + i] = from_float<T>(
-        fmaf(rstd, fmaf(-(to_float(h[i]) * rstd), c, to_float(dy[i]) * g), d));
+  const float c = -block_sum_max(SumMax{sum.x + sum.y, 0.f}, buf).sum / (float)a.m;
+  for (int p = 0; p < packs; ++p) {
+    const int first = first_of(p, head);
+    Floats d, u, r;
+    load(d, u, first);
+#pragma unroll
+    for (int k = 0; k < kPack / 2; ++k) r.v[k] = make_float2(0.f, 0.f);
+    if (a.dR != nullptr) r = floats_of(load8<false>(a.dR + j * a.lddr, first, a.m));
+#pragma unroll
+    for (int k = 0; k < kPack / 2; ++k)
+      d.v[k] = __ffma2_rn(rstd2, __ffma2_rn(u.v[k], make_float2(c, c), d.v[k]), r.v[k]);
+    store8<false>(dx, first, a.m, raw_of<T>(d));
   }
 }
 
-inline bool short_ld(int ld, int rows) { return ld < (rows > 1 ? rows : 1); }
+// ... and their dG, before dX may overwrite dY or H: block (x, y) sums 32 packs
+// of rows of dG over the y-th share of the columns
+constexpr int kTall = 16;
+template <class T>
+__global__ void __launch_bounds__(32 * kTall) rmsgrad_weight_kernel(RmsgradArgs<T> a, int share) {
+  __shared__ float buf[kTall][32 * kPack + 1];
+  await_predecessor();
+  const int first = ((int)blockIdx.x * 32 + (int)threadIdx.x) * kPack;
+  const long long end = min((long long)a.n, (blockIdx.y + 1LL) * share);
+  float2 s[kPack / 2];
+#pragma unroll
+  for (int k = 0; k < kPack / 2; ++k) s[k] = make_float2(0.f, 0.f);
+#pragma unroll 2
+  for (long long j = (long long)blockIdx.y * share + threadIdx.y; j < end; j += kTall) {
+    const float rstd = a.rstd[j];
+    const Floats d = floats_of(load8<false>(a.dY + j * a.lddy, first, a.m));
+    const Floats u = floats_of(load8<false>(a.H + j * a.ldh, first, a.m));
+#pragma unroll
+    for (int k = 0; k < kPack / 2; ++k)
+      s[k] = __ffma2_rn(d.v[k], __fmul2_rn(u.v[k], make_float2(rstd, rstd)), s[k]);
+  }
+#pragma unroll
+  for (int k = 0; k < kPack / 2; ++k) {
+    buf[threadIdx.y][threadIdx.x * kPack + 2 * k] = s[k].x;
+    buf[threadIdx.y][threadIdx.x * kPack + 2 * k + 1] = s[k].y;
+  }
+  __syncthreads();
+  const int at = (int)(threadIdx.y * 32 + threadIdx.x), i = (int)blockIdx.x * 32 * kPack + at;
+  if (at < 32 * kPack && i < a.m) {
+    float t = 0.f;
+#pragma unroll
+    for (int y = 0; y < kTall; ++y) t += buf[y][at];
+    a.parts[(long long)blockIdx.y * a.m + i] = t;
+  }
+}
+
+// dG = the sum of the `count` partial sums, m apart (count = 0: zero)
+__global__ void weight_sum_kernel(int m, int count, const float* parts, float* dG) {
+  __shared__ float buf[kTall][33];
+  await_predecessor();
+  const int i = blockIdx.x * 32 + threadIdx.x;
+  float s = 0.f;
+  if (i < m)
+#pragma unroll 4
+    for (int c = threadIdx.y; c < count; c += kTall) s += parts[(long long)c * m + i];
+  buf[threadIdx.y][threadIdx.x] = s;
+  __syncthreads();
+  if (threadIdx.y == 0 && i < m) {
+#pragma unroll
+    for (int y = 1; y < kTall; ++y) s += buf[y][threadIdx.x];
+    dG[i] = s;
+  }
+}
+
+// ------------------------------------------------------------------- host --
 
 bool device_ok() {
   int dev, sms;
   return current_device(&dev, &sms);
+}
+
+// the elements that packs may begin before a column: none if every column
+// starts on the grid its packs are laid on
+template <class T>
+int most_head(const T* p, long long ld) {
+  const bool on_grid = reinterpret_cast<uintptr_t>(p) % kPiece<T> == 0 &&
+                       (size_t)ld * sizeof(T) % kPiece<T> == 0;
+  return on_grid ? 0 : kPiece<T> / (int)sizeof(T) - 1;
+}
+
+// packs a thread (1, 2 or 4) and threads a block for columns of m elements; 0
+// packs: longer than the registers of `most` threads at 4 packs each.
+// Where there are columns for every SM several times over (n >= 2 sms), 64 bytes
+// a thread of each operand: small blocks, of which many fit on an SM, so that
+// some load while others reduce.  Else as few as possible: one column's latency.
+// Columns that a warp holds go four to a block: blocks of one warp start too
+// slowly (16384 columns of 1024 halves: 17 us against 7).
+struct Shape {
+  int packs, threads;
+  int columns(int n) const { return threads == 32 ? std::min(n, 4) : 1; }
+  dim3 block(int n) const { return dim3(threads, columns(n)); }
+  unsigned grid(int n) const { return (unsigned)((n + (long long)columns(n) - 1) / columns(n)); }
+};
+template <class T>
+Shape shape_for(int m, int n, int head, int most) {
+  int dev, sms = 1;
+  current_device(&dev, &sms);
+  const int all = (m + head + kPack - 1) / kPack;
+  for (int packs = n >= 2 * sms ? std::min(8 / (int)sizeof(T), std::max(1, all / 32)) : 1;
+       packs <= 4; packs *= 2) {
+    const int threads = ((all + packs - 1) / packs + 31) / 32 * 32;
+    if (threads <= most) return Shape{packs, threads};
+  }
+  return Shape{0, most};
 }
 
 template <class T>
@@ -165,8 +920,15 @@ int quant_entry(int m, int n, const T* X, int ldx, int8_t* Q, int ldq, float* sc
   if (m == 0 || n == 0) return XSYMV_OK;
   if (X == nullptr || Q == nullptr || scale == nullptr) return XSYMV_ERR_VALUE;
   if (!device_ok()) return XSYMV_ERR_DEVICE;
-  quant_kernel<T><<<n, kThreads, 0, current_stream()>>>(m, X, ldx, Q, ldq, scale);
-  return launched(cudaGetLastError(), 1);
+  cudaStream_t st = current_stream();
+  const Shape s = shape_for<T>(m, n, most_head(Q, ldq), 1024);
+  const bool g = m % kPack == 0 && most_head(X, ldx) == 0 && most_head(Q, ldq) == 0;
+  auto* kernel = s.packs == 1   ? (g ? quant_kernel<T, 1, true> : quant_kernel<T, 1, false>)
+                 : s.packs == 2 ? (g ? quant_kernel<T, 2, true> : quant_kernel<T, 2, false>)
+                 : s.packs == 4 ? (g ? quant_kernel<T, 4, true> : quant_kernel<T, 4, false>)
+                                : (g ? quant_kernel<T, 0, true> : quant_kernel<T, 0, false>);
+  return launched(launch_after(kernel, s.grid(n), s.block(n), 0, st, m, n, X, ldx, Q, ldq, scale), 1,
+                  st);
 }
 
 template <class T>
@@ -178,8 +940,18 @@ int dequant_entry(int m, int n, const int8_t* Q, int ldq, const float* scale, T*
   if (m == 0 || n == 0) return XSYMV_OK;
   if (X == nullptr || Q == nullptr || scale == nullptr) return XSYMV_ERR_VALUE;
   if (!device_ok()) return XSYMV_ERR_DEVICE;
-  dequant_kernel<T><<<n, kThreads, 0, current_stream()>>>(m, Q, ldq, scale, X, ldx);
-  return launched(cudaGetLastError(), 1);
+  cudaStream_t st = current_stream();
+  // 256 threads: as many along the column as have packs there, a power of two
+  int along = 1;
+  while (along < 256 && along * kDeep * kPack < m) along *= 2;
+  const long long step = (long long)along * kDeep * kPack;
+  const dim3 grid((unsigned)((n + 256LL / along - 1) / (256 / along)),
+                  (unsigned)std::min<long long>((m + most_head(X, ldx) + step - 1) / step, 65535));
+  const bool g = m % kPack == 0 && most_head(X, ldx) == 0 && most_head(Q, ldq) == 0;
+  auto* kernel = g ? dequant_kernel<T, true> : dequant_kernel<T, false>;
+  return launched(launch_after(kernel, grid, dim3(along, 256 / along), 0, st, m, n, Q,
+                               ldq, scale, X, ldx),
+                  1, st);
 }
 
 template <class T>
@@ -195,9 +967,39 @@ int rmsquant_entry(int m, int n, const T* X, int ldx, const T* R, int ldr, const
   if (m == 0 || n == 0) return XSYMV_OK;
   if (X == nullptr || Q == nullptr || scale == nullptr) return XSYMV_ERR_VALUE;
   if (!device_ok()) return XSYMV_ERR_DEVICE;
-  const RmsquantArgs<T> a{m, X, ldx, R, ldr, G, eps, H, ldh, Q, ldq, scale, rstd};
-  rmsquant_kernel<T><<<n, kThreads, 0, current_stream()>>>(a);
-  return launched(cudaGetLastError(), 1);
+  cudaStream_t st = current_stream();
+  const RmsquantArgs<T> a{m, n, X, ldx, R, ldr, G, eps, H, ldh, Q, ldq, scale, rstd};
+  const Shape s =
+      shape_for<T>(m, n, H != nullptr ? most_head(H, ldh) : most_head(Q, ldq), 1024);
+  const bool g = m % kPack == 0 && most_head(X, ldx) == 0 && most_head(Q, ldq) == 0 &&
+                 (R == nullptr || most_head(R, ldr) == 0) && most_head(G, 0) == 0 &&
+                 (H == nullptr || most_head(H, ldh) == 0);
+  auto* kernel =
+      s.packs == 1   ? (g ? rmsquant_kernel<T, 1, true> : rmsquant_kernel<T, 1, false>)
+      : s.packs == 2 ? (g ? rmsquant_kernel<T, 2, true> : rmsquant_kernel<T, 2, false>)
+      : s.packs == 4 ? (g ? rmsquant_kernel<T, 4, true> : rmsquant_kernel<T, 4, false>)
+                     : (g ? rmsquant_kernel<T, 0, true> : rmsquant_kernel<T, 0, false>);
+  return launched(launch_after(kernel, s.grid(n), s.block(n), 0, st, a), 1, st);
+}
+
+template <class T>
+struct GradKernel {
+  void (*run)(RmsgradArgs<T>, int);
+  int slots;
+};
+template <class T>
+GradKernel<T> grad_kernel(int packs, bool g) {
+  switch (packs) {
+    case 1:
+      return g ? GradKernel<T>{rmsgrad_kernel<T, 1, true>, kGradSlots<T, 1, true>}
+               : GradKernel<T>{rmsgrad_kernel<T, 1, false>, kGradSlots<T, 1, false>};
+    case 2:
+      return g ? GradKernel<T>{rmsgrad_kernel<T, 2, true>, kGradSlots<T, 2, true>}
+               : GradKernel<T>{rmsgrad_kernel<T, 2, false>, kGradSlots<T, 2, false>};
+    default:
+      return g ? GradKernel<T>{rmsgrad_kernel<T, 4, true>, kGradSlots<T, 4, true>}
+               : GradKernel<T>{rmsgrad_kernel<T, 4, false>, kGradSlots<T, 4, false>};
+  }
 }
 
 template <class T>
@@ -212,17 +1014,57 @@ int rmsgrad_entry(int m, int n, const T* dY, int lddy, const T* H, int ldh, cons
   if (m == 0 || (n == 0 && dG == nullptr)) return XSYMV_OK;
   if (n > 0 && (dY == nullptr || H == nullptr || rstd == nullptr || dX == nullptr))
     return XSYMV_ERR_VALUE;
-  if (!device_ok()) return XSYMV_ERR_DEVICE;
+  int dev, sms;
+  if (!current_device(&dev, &sms)) return XSYMV_ERR_DEVICE;
   cudaStream_t st = current_stream();
-  const RmsgradArgs<T> a{m, n, dY, lddy, H, ldh, G, rstd, dR, lddr, dX, lddx, dG};
-  if (dG != nullptr) {
-    rmsgrad_weight_kernel<T><<<(m + kThreads - 1) / kThreads, kThreads, 0, st>>>(a);
-    const int s = launched(cudaGetLastError(), 1);
-    if (s != XSYMV_OK) return s;
+  Shape s = shape_for<T>(m, n, 0, 512);
+  const bool g = m % kPack == 0 && most_head(dY, lddy) == 0 && most_head(H, ldh) == 0 &&
+                 most_head(G, 0) == 0 && (dR == nullptr || most_head(dR, lddr) == 0) &&
+                 most_head(dX, lddx) == 0;
+  const GradKernel<T> kernel = grad_kernel<T>(s.packs, g);
+  const long long stage_bytes = (long long)kernel.slots * 16 * s.threads;
+  if (stage_bytes > kSmemPerSm - kBlockSmem) s.packs = 0;
+  // Blocks that share the columns: as many as an SM holds at 512 threads (or of
+  // the long columns' dG shares of at least 64 columns), each with the
+  // stages that their share of its memory allows
+  const int per_sm = std::max(1, 512 / s.threads);
+  const int stages = (int)std::min<long long>(
+      kMostStages, std::max<long long>(1, (kSmemPerSm / per_sm - kBlockSmem) / stage_bytes));
+  const size_t smem = (size_t)(stages * stage_bytes);
+  const int blocks = s.packs > 0 ? (int)std::min<long long>(n, (long long)sms * per_sm)
+                                 : (int)std::min<long long>((n + 63LL) / 64, 65535);
+  float* parts = nullptr;
+  if (dG != nullptr && n > 0) {
+    int status = XSYMV_OK;
+    parts = static_cast<float*>(
+        workspace((size_t)blocks * m * sizeof(float), st, &status, kSlotPartials, nullptr));
+    if (parts == nullptr) return status;
   }
-  if (n == 0) return XSYMV_OK;
-  rmsgrad_kernel<T><<<n, kThreads, 0, st>>>(a);
-  return launched(cudaGetLastError(), 1);
+  const RmsgradArgs<T> a{m, n, dY, lddy, H, ldh, G, rstd, dR, lddr, dX, lddx, parts};
+  int kernels = 0;
+  cudaError_t e = cudaSuccess;
+  if (n > 0 && s.packs > 0) {
+    if (smem + kBlockSmem > 48 * 1024)   // more than a block gets unasked
+      e = cudaFuncSetAttribute(kernel.run, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e == cudaSuccess) e = launch_after(kernel.run, blocks, s.threads, smem, st, a, stages);
+    ++kernels;
+  } else if (n > 0) {
+    if (dG != nullptr) {
+      const int share = (n + blocks - 1) / blocks;
+      e = launch_after(rmsgrad_weight_kernel<T>, dim3((m + 32 * kPack - 1) / (32 * kPack), blocks),
+                       dim3(32, kTall), 0, st, a, share);
+      ++kernels;
+    }
+    if (e == cudaSuccess)
+      e = launch_after(rmsgrad_long_kernel<T>, n, 1024, 0, st, a);
+    ++kernels;
+  }
+  if (e == cudaSuccess && dG != nullptr) {
+    e = launch_after(weight_sum_kernel, (m + 31) / 32, dim3(32, kTall), 0, st, m,
+                     n > 0 ? blocks : 0, parts, dG);
+    ++kernels;
+  }
+  return launched(e, kernels, st);
 }
 
 template <class T, class C>

@@ -24,11 +24,14 @@ bool current_device(int* dev, int* sm_count);
 
 // buffer of at least `bytes` for (current device, stream, slot); nullptr and
 // *status set on failure.  Slot 0: the kernels' workspace; slot 1: device
-// copies of host operands for the host-buffer entry points.
+// copies of host operands for the host-buffer entry points; slots 2 and 3:
+// partial sums and 16-bit operands of the 8-bit linear-layer operators.
 // For slot 0 the first 256 bytes (the status header) are zeroed when the
 // buffer is allocated, and *epoch receives a fresh call number (> 0) that the
 // kernels write to the status word if they give up on a wait.
 // *capacity (if given) receives the buffer's allocated size (>= bytes).
+constexpr int kSlotPartials = 2;
+constexpr int kSlotOperands = 3;
 void* workspace(size_t bytes, cudaStream_t stream, int* status, int slot, int* epoch,
                 size_t* capacity = nullptr);
 

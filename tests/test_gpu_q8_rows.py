@@ -232,7 +232,8 @@ def run_rmsgrad(kind, m, n, dy, h, w, rstd, dr, dx, dg):
 
 
 @pytest.mark.parametrize("kind", ["s", "h", "b"])
-@pytest.mark.parametrize("m,n", SIZES + [(96, 1000), (1024, 700), (33, 5000), (8200, 333)])
+@pytest.mark.parametrize("m,n", SIZES + [(96, 1000), (1024, 700), (33, 5000), (8200, 333),
+                                         (4096, 400), (2048, 350), (16384, 310), (12000, 400)])
 def test_rmsgrad(kind, m, n):
     g = gen(5 * m + n)
     dt = DTYPES[kind]
