@@ -22,191 +22,11 @@
 namespace xsymv {
 namespace {
 
-constexpr int kPack = 8;
 constexpr int kWarps = 32;   // of a block, at most
 constexpr int kSmemPerSm = 227 * 1024;
 constexpr int kBlockSmem = 2048;   // a block's reserve and its reduction buffers
 
-// ------------------------------------------------------ a column's elements --
-
-// a pack as 32-bit words, and as four pairs of floats
-template <class T>
-struct Raw {
-  static constexpr int N = kPack * sizeof(T) / 4;
-  uint32_t w[N];
-};
-struct Floats {
-  float2 v[kPack / 2];
-};
-__device__ __forceinline__ Floats floats_of(const Raw<float>& r) {
-  Floats f;
-#pragma unroll
-  for (int k = 0; k < kPack / 2; ++k)
-    f.v[k] = make_float2(__uint_as_float(r.w[2 * k]), __uint_as_float(r.w[2 * k + 1]));
-  return f;
-}
-__device__ __forceinline__ Floats floats_of(const Raw<__half>& r) {
-  Floats f;
-#pragma unroll
-  for (int k = 0; k < kPack / 2; ++k)
-    f.v[k] = __half22float2(*reinterpret_cast<const __half2*>(&r.w[k]));
-  return f;
-}
-__device__ __forceinline__ Floats floats_of(const Raw<__nv_bfloat16>& r) {
-  Floats f;
-#pragma unroll
-  for (int k = 0; k < kPack / 2; ++k)
-    f.v[k] = make_float2(__uint_as_float(r.w[k] << 16), __uint_as_float(r.w[k] & 0xffff0000u));
-  return f;
-}
-template <class T>
-__device__ __forceinline__ Raw<T> raw_of(const Floats& f);
-template <>
-__device__ __forceinline__ Raw<float> raw_of<float>(const Floats& f) {
-  Raw<float> r;
-#pragma unroll
-  for (int k = 0; k < kPack / 2; ++k) {
-    r.w[2 * k] = __float_as_uint(f.v[k].x);
-    r.w[2 * k + 1] = __float_as_uint(f.v[k].y);
-  }
-  return r;
-}
-template <>
-__device__ __forceinline__ Raw<__half> raw_of<__half>(const Floats& f) {
-  Raw<__half> r;
-#pragma unroll
-  for (int k = 0; k < kPack / 2; ++k) {
-    const __half2 h = __float22half2_rn(f.v[k]);
-    r.w[k] = *reinterpret_cast<const uint32_t*>(&h);
-  }
-  return r;
-}
-template <>
-__device__ __forceinline__ Raw<__nv_bfloat16> raw_of<__nv_bfloat16>(const Floats& f) {
-  Raw<__nv_bfloat16> r;
-#pragma unroll
-  for (int k = 0; k < kPack / 2; ++k) {
-    const __nv_bfloat162 h = __float22bfloat162_rn(f.v[k]);
-    r.w[k] = *reinterpret_cast<const uint32_t*>(&h);
-  }
-  return r;
-}
-
-// bytes of the aligned pieces that packs of T are loaded and stored by
-template <class T>
-constexpr int kPiece = sizeof(T) == 1 ? 8 : 16;
-
-// elements between the 16-byte boundary (8-byte, of 8-bit elements) and `row`
-template <bool GRID, class T>
-__device__ __forceinline__ int head_of(const T* row) {
-  return GRID ? 0 : (int)(reinterpret_cast<uintptr_t>(row) % kPiece<T>) / (int)sizeof(T);
-}
-// first element of this thread's pack p; may lie before the column
-__device__ __forceinline__ int first_of(int p, int head) {
-  return (p * (int)blockDim.x + (int)threadIdx.x) * kPack - head;
-}
-
-template <class T>
-__device__ __forceinline__ void load_piece(uint32_t* w, uintptr_t at) {
-  if (kPiece<T> == 16) {
-    const uint4 v = *reinterpret_cast<const uint4*>(at);
-    w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
-  } else {
-    const uint2 v = *reinterpret_cast<const uint2*>(at);
-    w[0] = v.x, w[1] = v.y;
-  }
-}
-
-// w[0 .. N] := w[off / 4 ..] of N + 4 words (off < 16), or of N + 2 (off < 8)
-template <int N, int M>
-__device__ __forceinline__ void shift_words(uint32_t (&w)[M], unsigned off) {
-  if (M == N + 4 && (off & 8))
-#pragma unroll
-    for (int k = 0; k < N + 2; ++k) w[k] = w[k + (M == N + 4 ? 2 : 0)];
-  if (off & 4)
-#pragma unroll
-    for (int k = 0; k < N + 1; ++k) w[k] = w[k + 1];
-}
-
-// elements first .. first+7 of the m of `row`, zeros outside 0 .. m-1.
-// GRID: every operand's columns start on the grid of 16-byte pieces (8-byte
-// ones of 8-bit elements) and are whole packs long, the usual case: a pack
-// is all of the column or all outside, and no element is looked at singly
-// (rmsquant 1024 x 16384 halves: 23 us without, 14 us with it).
-template <bool GRID, class T>
-__device__ __forceinline__ Raw<T> load8(const T* row, int first, int m) {
-  constexpr int N = Raw<T>::N, P = kPiece<T> / 4;
-  Raw<T> r;
-  if (GRID) {
-#pragma unroll
-    for (int k = 0; k < N; ++k) r.w[k] = 0;
-    if (first < m)
-#pragma unroll
-      for (int k = 0; k < N; k += P)
-        load_piece<T>(r.w + k, reinterpret_cast<uintptr_t>(row + first) + 4 * k);
-  } else if (first >= 0 && first + kPack <= m) {
-    const uintptr_t at = reinterpret_cast<uintptr_t>(row + first);
-    const unsigned off = at % kPiece<T>;
-    if (off == 0) {
-#pragma unroll
-      for (int k = 0; k < N; k += P) load_piece<T>(r.w + k, at + 4 * k);
-    } else {
-      // the pieces around the pack (each holds at least one of its elements)
-      uint32_t w[N + P];
-#pragma unroll
-      for (int k = 0; k < N + P; k += P) load_piece<T>(w + k, at - off + 4 * k);
-      shift_words<N>(w, off);
-#pragma unroll
-      for (int k = 0; k < N; ++k)
-        r.w[k] = sizeof(T) == 4 ? w[k] : __funnelshift_r(w[k], w[k + 1], (off & 3) * 8);
-    }
-  } else {
-#pragma unroll
-    for (int k = 0; k < N; ++k) r.w[k] = 0;
-#pragma unroll
-    for (int e = 0; e < kPack; ++e)
-      if (first + e >= 0 && first + e < m) {
-        uint32_t b;
-        if (sizeof(T) == 4)
-          b = *reinterpret_cast<const uint32_t*>(row + first + e);
-        else if (sizeof(T) == 2)
-          b = *reinterpret_cast<const uint16_t*>(row + first + e);
-        else
-          b = *reinterpret_cast<const uint8_t*>(row + first + e);
-        r.w[e * sizeof(T) / 4] |= b << (e * sizeof(T) % 4 * 8);
-      }
-  }
-  return r;
-}
-
-// elements first .. first+7 of `row`, those within 0 .. m-1
-template <bool GRID, class T>
-__device__ __forceinline__ void store8(T* row, int first, int m, const Raw<T>& r) {
-  constexpr int N = Raw<T>::N, P = kPiece<T> / 4;
-  const uintptr_t at = reinterpret_cast<uintptr_t>(row) + (long long)first * (int)sizeof(T);
-  if (GRID ? first < m : first >= 0 && first + kPack <= m && at % kPiece<T> == 0) {
-#pragma unroll
-    for (int k = 0; k < N; k += P) {
-      if (P == 4)
-        *reinterpret_cast<uint4*>(at + 4 * k) =
-            make_uint4(r.w[k], r.w[k + 1], r.w[(k + 2) % N], r.w[(k + 3) % N]);
-      else
-        *reinterpret_cast<uint2*>(at + 4 * k) = make_uint2(r.w[k], r.w[k + 1]);
-    }
-  } else if (!GRID) {
-#pragma unroll
-    for (int e = 0; e < kPack; ++e)
-      if (first + e >= 0 && first + e < m) {
-        const uint32_t b = r.w[e * sizeof(T) / 4] >> (e * sizeof(T) % 4 * 8);
-        if (sizeof(T) == 4)
-          *reinterpret_cast<uint32_t*>(row + first + e) = b;
-        else if (sizeof(T) == 2)
-          *reinterpret_cast<uint16_t*>(row + first + e) = (uint16_t)b;
-        else
-          *reinterpret_cast<uint8_t*>(row + first + e) = (uint8_t)b;
-      }
-  }
-}
+// ---------------------------------------------------------- a warp's store --
 
 // store8 of a warp's 32 packs in a row, all lanes at once.  Off the 16-byte
 // grid every lane writes the aligned pieces that begin in the previous
