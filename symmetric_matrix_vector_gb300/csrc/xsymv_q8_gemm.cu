@@ -16,18 +16,38 @@ __global__ void __launch_bounds__(256) scale_kernel(GemmqArgs<T> a) {
       store_output(a, i, j, 0.f, 0.f, 0.f);
 }
 
-// One output per thread, a 32 x 8 tile of (channel, token) per block; sums in
-// 64-bit integers.
-template <class T>
-__global__ void gemmq_kernel(GemmqArgs<T> a) {
-  await_predecessor();
-  const long long i = blockIdx.x * 32LL + threadIdx.x;
-  for (long long j = blockIdx.y * 8LL + threadIdx.y; j < a.n; j += gridDim.y * 8LL) {
-    if (i >= a.m) return;
-    long long acc = 0;
-    for (int p = 0; p < a.k; ++p) acc += (int)a.W[i * a.ldw + p] * (int)a.X[j * a.ldx + p];
-    store_output(a, i, j, (float)acc, channel_factor(a, i), token_factor(a, j));
-  }
+// ------------------------------------------------------------ a few tokens --
+
+template <int NT, int R>
+cudaError_t launch_dot(const GemmqAny& a, bool g, int sms, cudaStream_t st) {
+  // threads a row: 4 pieces of 16 integers a thread where that fills the SMs, else
+  // fewer pieces, down to one
+  int threads = 4;
+  while (threads < kDotBlock &&
+         (threads * 64 < a.k ||
+          (threads * 16 < a.k && (long long)a.m * threads / R < (long long)sms * 1024)))
+    threads *= 2;
+  while (threads > 32 && (long long)a.m * threads / R > (long long)sms * 8192) threads /= 2;
+  const long long rows = (long long)(kDotBlock / threads) * R;
+  return launch_after(g ? gemmq_dot<NT, R, true> : gemmq_dot<NT, R, false>,
+                      (unsigned)((a.m + rows - 1) / rows), kDotBlock, 0, st, a, threads);
+}
+
+cudaError_t launch_few(const GemmqAny& a, int sms, cudaStream_t st) {
+  auto on_grid = [](const int8_t* p, long long ld) {
+    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % 16 == 0;
+  };
+  const bool g = a.k % 16 == 0 && on_grid(a.W, a.ldw) && on_grid(a.X, a.ldx);
+  if (a.n == 1) return launch_dot<1, 1>(a, g, sms, st);
+  if (a.n == 2) return launch_dot<2, 2>(a, g, sms, st);
+  if (a.n <= 4) return launch_dot<4, 2>(a, g, sms, st);
+  auto* kernel = a.n <= 8    ? (g ? gemmq_mma<1, true> : gemmq_mma<1, false>)
+                 : a.n <= 16 ? (g ? gemmq_mma<2, true> : gemmq_mma<2, false>)
+                 : a.n <= 24 ? (g ? gemmq_mma<3, true> : gemmq_mma<3, false>)
+                 : a.n <= 32 ? (g ? gemmq_mma<4, true> : gemmq_mma<4, false>)
+                             : (g ? gemmq_mma<5, true> : gemmq_mma<5, false>);
+  return launch_after(kernel, (unsigned)((a.m + kMmaRows - 1LL) / kMmaRows), kMmaWarps * 32, 0, st,
+                      a);
 }
 
 // ------------------------------------------------------------ tensor cores --
@@ -125,7 +145,7 @@ int gemmq_tiled(const GemmqArgs<T>& a, int sms, cudaStream_t st) {
 }
 
 template <class T>
-int gemmq_entry(int m, int n, int k, float alpha, const int8_t* W, int ldw, const float* sw,
+int gemmq_entry(char type, int m, int n, int k, float alpha, const int8_t* W, int ldw, const float* sw,
                 const int8_t* X, int ldx, const float* sx, float beta, T* Y, int ldy) {
   if (m < 0) return 1;
   if (n < 0) return 2;
@@ -145,9 +165,12 @@ int gemmq_entry(int m, int n, int k, float alpha, const int8_t* W, int ldw, cons
     return launched(launch_after(scale_kernel<T>, dim3((m + 255) / 256, std::min(n, 65535)), 256, 0,
                                  st, a),
                     1, st);
-  if (n <= 32) {
-    const dim3 grid((m + 31) / 32, (unsigned)std::min((n + 7LL) / 8, 65535LL));
-    return launched(launch_after(gemmq_kernel<T>, grid, dim3(32, 8), 0, st, a), 1, st);
+  if (n <= 40 && k <= kDotMostDepth) {
+    GemmqAny any;
+    static_cast<GemmqArgs<void>&>(any) =
+        GemmqArgs<void>{m, n, k, alpha, W, ldw, sw, X, ldx, sx, beta, Y, ldy};
+    any.type = type;
+    return launched(launch_few(any, sms, st), 1, st);
   }
   if (n <= 64) return gemmq_tiled<T, 1, 64>(a, sms, st);
   if (n <= 128) return gemmq_tiled<T, 1, 128>(a, sms, st);
@@ -161,7 +184,7 @@ int gemmq_entry(int m, int n, int k, float alpha, const int8_t* W, int ldw, cons
   extern "C" XSYMV_API int xgemmq_##K(int m, int n, int k, float alpha, const signed char* W,   \
                                       int ldw, const float* sw, const signed char* X, int ldx,  \
                                       const float* sx, float beta, C* Y, int ldy) {             \
-    return xsymv::gemmq_entry<T>(m, n, k, alpha, W, ldw, sw, X, ldx, sx, beta,                  \
+    return xsymv::gemmq_entry<T>(#K[0], m, n, k, alpha, W, ldw, sw, X, ldx, sx, beta,                  \
                                  reinterpret_cast<T*>(Y), ldy);                                 \
   }
 

@@ -7,6 +7,8 @@
 // sums stay below 2^24.
 #pragma once
 
+#include <type_traits>
+
 #include "xsymv_q8.cuh"
 #include "xsymv_tensor.cuh"
 
@@ -46,6 +48,28 @@ __device__ __forceinline__ void store_output(const GemmqArgs<T>& a, long long i,
   *y = from_float<T>(v);
 }
 
+// ... with the type of Y known at run time, for the kernels of a few tokens
+struct GemmqAny : GemmqArgs<void> {
+  char type;   // 's', 'h' or 'b'
+};
+__device__ __forceinline__ void store_any(const GemmqAny& a, long long i, long long j, float acc) {
+  const float channel = a.sw != nullptr ? a.sw[i] : 1.f;
+  const float token = (a.sx != nullptr ? a.sx[j] : 1.f) * a.alpha;
+  auto put = [&](auto* y) {
+    using T = std::remove_pointer_t<decltype(y)>;
+    float v = acc * channel * token;
+    if (a.beta != 0.f) v = fmaf(a.beta, to_float(*y), v);
+    *y = from_float<T>(v);
+  };
+  const long long at = j * a.ldy + i;
+  if (a.type == 's')
+    put(static_cast<float*>(a.Y) + at);
+  else if (a.type == 'h')
+    put(static_cast<__half*>(a.Y) + at);
+  else
+    put(static_cast<__nv_bfloat16*>(a.Y) + at);
+}
+
 // four 8-bit integers as halves: xor 128 makes them 0 .. 255, which set into the
 // low bits of 1024 (0x6400) read 1024 + v + 128
 __device__ __forceinline__ void halves_of(uint32_t q, uint32_t& lo, uint32_t& hi) {
@@ -56,6 +80,226 @@ __device__ __forceinline__ void halves_of(uint32_t q, uint32_t& lo, uint32_t& hi
   __half2 hb = __hsub2(*reinterpret_cast<__half2*>(&b), bias);
   lo = *reinterpret_cast<uint32_t*>(&ha);
   hi = *reinterpret_cast<uint32_t*>(&hb);
+}
+
+// ---------------------------------------------------------- a few tokens --
+
+// 16 integers first .. first+15 of the k of `row` (first a multiple of 16), at any
+// alignment.  GRID: rows start on 16-byte boundaries and are multiples of 16
+// long.  MASK: those beyond k are zero; else they are any integers (their
+// partners are zero).  Only 16-byte pieces that hold an element of the row are
+// read.
+__device__ __forceinline__ uint4 load_once(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+template <bool GRID, bool MASK>
+__device__ __forceinline__ uint4 load16(const int8_t* row, int first, int k) {
+  uint4 z = make_uint4(0, 0, 0, 0);
+  if (first >= k) return z;
+  const int8_t* at = row + first;
+  // X is read by many warps, W once
+  auto piece = [](const void* p) {
+    return MASK ? __ldg(reinterpret_cast<const uint4*>(p)) : load_once(p);
+  };
+  if (GRID) return piece(at);
+  const unsigned off = (unsigned)(reinterpret_cast<uintptr_t>(at) % 16);
+  const uint4 a = piece(at - off);
+  if (off == 0) {
+    z = a;
+  } else {
+    uint4 b = z;
+    if (at - off + 16 < row + k) b = piece(at - off + 16);
+    uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    shift_words<4>(w, off);
+    const unsigned bits = (off & 3) * 8;
+    z = make_uint4(__funnelshift_r(w[0], w[1], bits), __funnelshift_r(w[1], w[2], bits),
+                   __funnelshift_r(w[2], w[3], bits), __funnelshift_r(w[3], w[4], bits));
+  }
+  if (MASK && first + 16 > k) {
+    const int left = k - first;   // 1 .. 15
+    auto keep = [&](uint32_t v, int at) {
+      return left >= at + 4 ? v : left <= at ? 0u : v & ((1u << 8 * (left - at)) - 1u);
+    };
+    z = make_uint4(keep(z.x, 0), keep(z.y, 4), keep(z.z, 8), keep(z.w, 12));
+  }
+  return z;
+}
+
+// Up to 4 tokens: dot products of 8-bit integers (dp4a, 32-bit sums), bound
+// by the bytes of W.  A row of W (a channel) is `threads` threads' work, a power of
+// two from 4 to a whole block, R rows at a time; X comes from L1.
+constexpr int kDotBlock = 256;
+constexpr int kDotMostDepth = 1 << 22;   // a thread's sums stay below 2^31
+template <int NT, int R, bool GRID>
+__global__ void __launch_bounds__(kDotBlock) gemmq_dot(GemmqAny a, int threads) {
+  __shared__ float buf[kDotBlock / 32][R * NT];
+  await_predecessor();
+  const int part = (int)threadIdx.x & (threads - 1);
+  const long long i0 = ((long long)blockIdx.x * (kDotBlock / threads) + threadIdx.x / threads) * R;
+  int acc[R][NT];
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int t = 0; t < NT; ++t) acc[r][t] = 0;
+  const int8_t *w[R], *x[NT];
+#pragma unroll
+  for (int r = 0; r < R; ++r) w[r] = a.W + min(i0 + r, a.m - 1LL) * a.ldw;
+#pragma unroll
+  for (int t = 0; t < NT; ++t) x[t] = a.X + min(t, a.n - 1) * a.ldx;
+  constexpr int U = 4 / R;   // 64 bytes of W on their way
+  for (int p = part * 16; p < a.k; p += threads * 16 * U) {
+    uint4 q[U][R];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int r = 0; r < R; ++r) q[u][r] = load16<GRID, false>(w[r], p + u * threads * 16, a.k);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        const uint4 v = load16<GRID, true>(x[t], p + u * threads * 16, a.k);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          acc[r][t] = __dp4a((int)q[u][r].x, (int)v.x, acc[r][t]);
+          acc[r][t] = __dp4a((int)q[u][r].y, (int)v.y, acc[r][t]);
+          acc[r][t] = __dp4a((int)q[u][r].z, (int)v.z, acc[r][t]);
+          acc[r][t] = __dp4a((int)q[u][r].w, (int)v.w, acc[r][t]);
+        }
+      }
+  }
+  // sums below 2^31 are added as integers, larger ones (k >= 2^17) as floats
+  const bool whole = a.k < 1 << 17;
+  float sum[R][NT];
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      if (whole) {
+        int v = acc[r][t];
+        for (int o = min(threads, 32) / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+        sum[r][t] = __int_as_float(v);
+      } else {
+        float v = (float)acc[r][t];
+        for (int o = min(threads, 32) / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+        sum[r][t] = v;
+      }
+    }
+  if (threads > 32) {
+    if (threadIdx.x % 32 == 0)
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int t = 0; t < NT; ++t) buf[threadIdx.x / 32][r * NT + t] = sum[r][t];
+    __syncthreads();
+  }
+  if (part != 0) return;
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      if (i0 + r >= a.m || t >= a.n) continue;
+      float v;
+      if (whole) {
+        int s = __float_as_int(sum[r][t]);
+        for (int w = 1; w < threads / 32; ++w)
+          s += __float_as_int(buf[threadIdx.x / 32 + w][r * NT + t]);
+        v = (float)s;
+      } else {
+        v = sum[r][t];
+        for (int w = 1; w < threads / 32; ++w) v += buf[threadIdx.x / 32 + w][r * NT + t];
+      }
+      store_any(a, i0 + r, t, v);
+    }
+}
+
+// 5 to 40 tokens: W and X become halves in registers, products on the
+// warp-level tensor path (mma.sync, m16n8k16), whose 1000 multiply-adds a clock and SM
+// keep up with the bytes of W up to about 40 tokens; above, tiles win.  A lane holds
+// 16 consecutive integers of the rows g and g + 8 of a 16-row tile (g =
+// lane / 4) and of token g: the depth is taken in whatever order makes them
+// fragments, the same for W and X.  A warp has 2 row tiles and every 8th
+// part of the depth; the block's 8 warps add their sums in shared memory, in
+// warp order.
+constexpr int kMmaWarps = 8, kMmaRows = 32;
+__device__ __forceinline__ void mma_16x8x16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                            uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+template <int NT8, bool GRID>
+__global__ void __launch_bounds__(kMmaWarps * 32) gemmq_mma(GemmqAny a) {
+  __shared__ float buf[kMmaWarps][kMmaRows][NT8 * 8 + 2];
+  await_predecessor();
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
+  const long long i0 = (long long)blockIdx.x * kMmaRows;
+  const int8_t *w[4], *x[NT8];
+#pragma unroll
+  for (int r = 0; r < 4; ++r) w[r] = a.W + min(i0 + g + 8 * r, a.m - 1LL) * a.ldw;
+#pragma unroll
+  for (int c = 0; c < NT8; ++c) x[c] = a.X + min(g + 8 * c, a.n - 1) * a.ldx;
+  float acc[2][NT8][4];
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int c = 0; c < NT8; ++c)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[h][c][e] = 0.f;
+  uint4 next[4];
+  const int step = kMmaWarps * 64;
+  int p = warp * 64 + t * 16;
+#pragma unroll
+  for (int r = 0; r < 4; ++r) next[r] = load16<GRID, false>(w[r], p, a.k);
+  for (; p - t * 16 < a.k; p += step) {
+    uint4 q[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      q[r] = next[r];
+      next[r] = load16<GRID, false>(w[r], p + step, a.k);
+    }
+    uint4 v[NT8];
+#pragma unroll
+    for (int c = 0; c < NT8; ++c) v[c] = load16<GRID, true>(x[c], p, a.k);
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {   // 4 of the lane's 16 integers
+      auto word = [s](const uint4& u) { return s == 0 ? u.x : s == 1 ? u.y : s == 2 ? u.z : u.w; };
+      uint32_t lo[4], hi[4];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) halves_of(word(q[r]), lo[r], hi[r]);
+#pragma unroll
+      for (int c = 0; c < NT8; ++c) {
+        uint32_t b0, b1;
+        halves_of(word(v[c]), b0, b1);
+        mma_16x8x16(acc[0][c], lo[0], lo[1], hi[0], hi[1], b0, b1);
+        mma_16x8x16(acc[1][c], lo[2], lo[3], hi[2], hi[3], b0, b1);
+      }
+    }
+  }
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int c = 0; c < NT8; ++c) {
+      float* b = &buf[warp][h * 16 + g][c * 8 + 2 * t];
+      b[0] = acc[h][c][0];
+      b[1] = acc[h][c][1];
+      b += 8 * (NT8 * 8 + 2);
+      b[0] = acc[h][c][2];
+      b[1] = acc[h][c][3];
+    }
+  __syncthreads();
+  // lanes along the channels
+  for (int c = warp; c < a.n; c += kMmaWarps) {
+    float v = 0.f;
+#pragma unroll
+    for (int s = 0; s < kMmaWarps; ++s) v += buf[s][lane][c];
+    if (i0 + lane < a.m) store_any(a, i0 + lane, c, v);
+  }
 }
 
 // ------------------------------------------------------ operands as halves --
