@@ -16,6 +16,9 @@ __global__ void __launch_bounds__(256) scale_kernel(GemmqArgs<T> a) {
       store_output(a, i, j, 0.f, 0.f, 0.f);
 }
 
+
+constexpr int kFewTokens = 8;
+constexpr int kStreamTokens = 1024;
 // ------------------------------------------------------------ a few tokens --
 
 template <int NT, int R>
@@ -71,31 +74,128 @@ EncodeTiled encoder() {
   return fn;
 }
 
-// rows of `width` halves in boxes of kDepth halves by `box_rows` rows, zeros
-// outside; base 256-byte aligned, width a multiple of kDepth
-bool map_halves(CUtensorMap* map, __half* base, long long width, long long rows, int box_rows) {
+// `rows` rows of `width` elements, `pitch` bytes apart, in boxes of 128 bytes by
+// box_rows rows under the 128-byte swizzle, zeros outside; base and pitch multiples of
+// 16 bytes
+bool map_rows(CUtensorMap* map, CUtensorMapDataType type, int bytes, const void* base,
+              long long width, long long rows, long long pitch, int box_rows) {
   const EncodeTiled encode = encoder();
   if (encode == nullptr) return false;
   const cuuint64_t size[2] = {(cuuint64_t)width, (cuuint64_t)rows};
-  const cuuint64_t pitch[1] = {(cuuint64_t)width * sizeof(__half)};
-  const cuuint32_t box[2] = {(cuuint32_t)kDepth, (cuuint32_t)box_rows};
+  const cuuint64_t pitches[1] = {(cuuint64_t)pitch};
+  const cuuint32_t box[2] = {128u / (cuuint32_t)bytes, (cuuint32_t)box_rows};
   const cuuint32_t step[2] = {1, 1};
-  return encode(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, base, size, pitch, box, step,
+  return encode(map, type, 2, const_cast<void*>(base), size, pitches, box, step,
                 CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                 CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+bool map_halves(CUtensorMap* map, const __half* base, long long width, long long rows,
+                int box_rows) {
+  return map_rows(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, base, width, rows, width * 2, box_rows);
+}
+
+// blocks of 256 threads, a power of two of them along a row of `width` packs
+dim3 pack_block(long long width) {
+  unsigned along = 8;
+  while (along < 256 && along < width) along *= 2;
+  return dim3(along, 256 / along);
+}
+dim3 pack_grid(long long rows, long long width, dim3 block) {
+  return dim3((unsigned)((rows + block.y - 1) / block.y),
+              (unsigned)std::min<long long>((width + block.x - 1) / block.x, 65535));
 }
 
 cudaError_t launch_halves(int rows, int k, int kp, const int8_t* q, long long ldq, __half* out,
                           cudaStream_t st) {
   const bool g = k % kPack == 0 && reinterpret_cast<uintptr_t>(q) % 8 == 0 && ldq % 8 == 0;
-  int along = 8;
-  while (along < 256 && along * kPack < kp) along *= 2;
-  const long long by = 256 / along, step = (long long)along * kPack;
-  const dim3 grid((unsigned)((rows + by - 1) / by),
-                  (unsigned)std::min<long long>((kp + step - 1) / step, 65535));
-  return launch_after(g ? halves_kernel<true> : halves_kernel<false>, grid,
-                      dim3(along, (unsigned)by), 0, st, rows, k, kp, q, ldq, out);
+  const dim3 block = pack_block(kp / kPack);
+  return launch_after(g ? halves_kernel<true> : halves_kernel<false>,
+                      pack_grid(rows, kp / kPack, block), block, 0, st, rows, k, kp, q, ldq, out);
+}
+
+// a workspace cut into pieces on 256-byte boundaries
+struct Pieces {
+  size_t bytes = 0;
+  size_t add(size_t size) {
+    const size_t at = bytes;
+    bytes += (size + 255) / 256 * 256;
+    return at;
+  }
+};
+
+// The shared end of the two tensor-core forms: launch with clusters of `cluster`
+// CTAs, record the status word that the kernel's bounded waits write
+template <class... P, class... A>
+cudaError_t launch_cluster(void (*kernel)(P...), unsigned grid, int cluster, int threads, int smem,
+                           cudaStream_t st, A... args) {
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
+
+int* status_word(cudaStream_t st, int* status, int* epoch) {
+  return static_cast<int*>(workspace(256, st, status, 0, epoch));
+}
+
+template <int CTAS, int BN>
+int gemmq_streamed(const GemmqAny& a, int sms, cudaStream_t st) {
+  using S = Stream<CTAS, BN>;
+  const int steps = (int)((a.k + (long long)kStepDepth - 1) / kStepDepth);
+  const long long kp = (long long)steps * kStepDepth;
+  const bool on_grid = reinterpret_cast<uintptr_t>(a.W) % 16 == 0 && a.ldw % 16 == 0;
+  const long long ldo = (a.k + 15LL) / 16 * 16;
+  Pieces pieces;
+  const size_t at_x = pieces.add((size_t)a.n * kp * 2);
+  const size_t at_w = on_grid ? 0 : pieces.add((size_t)a.m * ldo);
+  int status = XSYMV_OK, epoch = 0;
+  int* const word = status_word(st, &status, &epoch);
+  if (word == nullptr) return status;
+  char* ws = static_cast<char*>(workspace(pieces.bytes, st, &status, kSlotOperands, nullptr));
+  if (ws == nullptr) return status;
+  __half* const x = reinterpret_cast<__half*>(ws + at_x);
+  const int8_t* const w = on_grid ? a.W : reinterpret_cast<int8_t*>(ws + at_w);
+  CUtensorMap map_w, map_x;
+  if (!map_rows(&map_w, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, w, a.k, a.m, on_grid ? a.ldw : ldo, 128) ||
+      !map_halves(&map_x, x, kp, a.n, BN / CTAS))
+    return XSYMV_ERR_CUDA;
+  int kernels = 2;
+  cudaError_t e = cudaSuccess;
+  if (!on_grid) {
+    const dim3 block = pack_block(ldo / kPack);
+    e = launch_after(align_kernel, pack_grid(a.m, ldo / kPack, block), block, 0, st, a.m, a.k, a.W,
+                     a.ldw, reinterpret_cast<int8_t*>(ws + at_w), ldo);
+    ++kernels;
+  }
+  if (e == cudaSuccess) e = launch_halves(a.n, a.k, (int)kp, a.X, a.ldx, x, st);
+  if (e == cudaSuccess) {
+    const long long tiles_m = (a.m + S::kChannels - 1LL) / S::kChannels;
+    const long long tiles_n = (a.n + BN - 1LL) / BN;
+    int split = 1;
+    while (CTAS == 1 && split < 8 && split * 2 <= steps &&
+           tiles_m * tiles_n * split * 2 <= (S::kTwice ? 2LL : 1LL) * sms)
+      split *= 2;
+    const int cluster = CTAS == 2 ? 2 : split;
+    e = launch_cluster(gemmq_stream<CTAS, BN>, (unsigned)(tiles_m * tiles_n * cluster), cluster,
+                       S::kThreads, S::kSmem, st, map_w, map_x, a, (int)tiles_n, steps, split, word,
+                       epoch, wait_limit_ns(), test_extra_tx());
+  }
+  const int r = launched(e, kernels, st);
+  if (r == XSYMV_OK) note_call_status(st, word, epoch);
+  return r;
 }
 
 template <class T, int CTAS, int BN>
@@ -103,41 +203,28 @@ int gemmq_tiled(const GemmqArgs<T>& a, int sms, cudaStream_t st) {
   using S = Tile<CTAS, BN>;
   const int steps = (int)((a.k + (long long)kDepth - 1) / kDepth), kp = steps * kDepth;
   int status = XSYMV_OK, epoch = 0;
-  int* word = static_cast<int*>(workspace(256, st, &status, 0, &epoch));
+  int* const word = status_word(st, &status, &epoch);
   if (word == nullptr) return status;
-  const size_t bytes_w = ((size_t)a.m * kp * 2 + 255) / 256 * 256, bytes_x = (size_t)a.n * kp * 2;
-  char* ws = static_cast<char*>(workspace(bytes_w + bytes_x, st, &status, kSlotOperands, nullptr));
+  Pieces pieces;
+  const size_t at_w = pieces.add((size_t)a.m * kp * 2), at_x = pieces.add((size_t)a.n * kp * 2);
+  char* ws = static_cast<char*>(workspace(pieces.bytes, st, &status, kSlotOperands, nullptr));
   if (ws == nullptr) return status;
-  __half* const w = reinterpret_cast<__half*>(ws);
-  __half* const x = reinterpret_cast<__half*>(ws + bytes_w);
+  __half* const w = reinterpret_cast<__half*>(ws + at_w);
+  __half* const x = reinterpret_cast<__half*>(ws + at_x);
   CUtensorMap map_w, map_x;
   if (!map_halves(&map_w, w, kp, a.m, 128) || !map_halves(&map_x, x, kp, a.n, BN / CTAS))
     return XSYMV_ERR_CUDA;
   cudaError_t e = launch_halves(a.m, a.k, kp, a.W, a.ldw, w, st);
   if (e == cudaSuccess) e = launch_halves(a.n, a.k, kp, a.X, a.ldx, x, st);
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(gemmq_tiles<T, CTAS, BN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             S::kSmem);
   if (e == cudaSuccess) {
     TileOrder order;
     order.tiles_m = (a.m + S::kChannels - 1) / S::kChannels;
     order.tiles_n = (a.n + BN - 1) / BN;
     order.tiles = order.tiles_m * order.tiles_n;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(CTAS * std::min(order.tiles, sms / CTAS)));
-    cfg.blockDim = dim3(S::kThreads);
-    cfg.dynamicSmemBytes = S::kSmem;
-    cfg.stream = st;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = CTAS;
-    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    e = cudaLaunchKernelEx(&cfg, gemmq_tiles<T, CTAS, BN>, map_w, map_x, a, order, steps, word,
-                           epoch, wait_limit_ns(), test_extra_tx());
+    e = launch_cluster(gemmq_tiles<T, CTAS, BN>,
+                       (unsigned)(CTAS * std::min(order.tiles, sms / CTAS)), CTAS, S::kThreads,
+                       S::kSmem, st, map_w, map_x, a, order, steps, word, epoch, wait_limit_ns(),
+                       test_extra_tx());
   }
   const int r = launched(e, 3, st);
   if (r == XSYMV_OK) note_call_status(st, word, epoch);
@@ -165,15 +252,17 @@ int gemmq_entry(char type, int m, int n, int k, float alpha, const int8_t* W, in
     return launched(launch_after(scale_kernel<T>, dim3((m + 255) / 256, std::min(n, 65535)), 256, 0,
                                  st, a),
                     1, st);
-  if (n <= 40 && k <= kDotMostDepth) {
-    GemmqAny any;
-    static_cast<GemmqArgs<void>&>(any) =
-        GemmqArgs<void>{m, n, k, alpha, W, ldw, sw, X, ldx, sx, beta, Y, ldy};
-    any.type = type;
+  GemmqAny any;
+  static_cast<GemmqArgs<void>&>(any) =
+      GemmqArgs<void>{m, n, k, alpha, W, ldw, sw, X, ldx, sx, beta, Y, ldy};
+  any.type = type;
+  if (n <= kFewTokens && k <= kDotMostDepth)
     return launched(launch_few(any, sms, st), 1, st);
-  }
-  if (n <= 64) return gemmq_tiled<T, 1, 64>(a, sms, st);
-  if (n <= 128) return gemmq_tiled<T, 1, 128>(a, sms, st);
+  if (n <= 16) return gemmq_streamed<1, 16>(any, sms, st);
+  if (n <= 32) return gemmq_streamed<1, 32>(any, sms, st);
+  if (n <= 64) return gemmq_streamed<1, 64>(any, sms, st);
+  if (n <= 128) return gemmq_streamed<1, 128>(any, sms, st);
+  if (n <= kStreamTokens) return gemmq_streamed<2, 256>(any, sms, st);
   return gemmq_tiled<T, 2, 256>(a, sms, st);
 }
 

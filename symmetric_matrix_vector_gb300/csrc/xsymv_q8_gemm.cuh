@@ -306,7 +306,7 @@ __global__ void __launch_bounds__(kMmaWarps * 32) gemmq_mma(GemmqAny a) {
 
 // Rows of kp halves (a multiple of kDepth, zeros beyond k) from rows of k
 // integers at any alignment: what the tensor copies read.
-constexpr int kDepth = 64;   // of a stage: 128 bytes of halves
+constexpr int kDepth = 64;   // 128 bytes of halves
 template <bool GRID>
 __global__ void __launch_bounds__(256) halves_kernel(int rows, int k, int kp, const int8_t* q,
                                                      long long ldq, __half* out) {
@@ -322,6 +322,21 @@ __global__ void __launch_bounds__(256) halves_kernel(int rows, int k, int kp, co
     halves_of(r.w[0], h.x, h.y);
     halves_of(r.w[1], h.z, h.w);
     *reinterpret_cast<uint4*>(out + first) = h;
+  }
+}
+
+// ... and rows of 8-bit integers on 16-byte boundaries, ldo a multiple of 16
+__global__ void __launch_bounds__(256) align_kernel(int rows, int k, const int8_t* q, long long ldq,
+                                                    int8_t* out, long long ldo) {
+  await_predecessor();
+  const long long j = blockIdx.x * (long long)blockDim.y + threadIdx.y;
+  if (j >= rows) return;
+  q += j * ldq;
+  out += j * ldo;
+  for (int first = (int)(blockIdx.y * blockDim.x + threadIdx.x) * kPack; first < ldo;
+       first += (int)(gridDim.y * blockDim.x) * kPack) {
+    const Raw<int8_t> r = load8<false>(q, first, k);
+    *reinterpret_cast<uint2*>(out + first) = make_uint2(r.w[0], r.w[1]);
   }
 }
 
@@ -508,6 +523,273 @@ __global__ void __launch_bounds__(192, 1)
   if (CTAS == 2) cluster_sync();
   tensor_fence_after();
   if (warp == 1) tmem_free<CTAS>(tmem, S::kColumns);
+}
+
+// ------------------------------------------- tiles with W as it is stored --
+
+// From 9 tokens to a few thousand, where converting W beforehand would cost more than
+// the product: W reaches shared memory as 8-bit integers, eight warps make
+// halves of it on the way to tensor memory, and the tensor cores take their
+// first operand from there.  (In shared memory the halves would cost four
+// times their 8-bit bytes of its bandwidth, more than an SM has at the rate W
+// streams in.)  One tile a CTA, or 256 x 256 a pair; small shapes fit twice on an
+// SM, so that one's ends overlap the other's middle.  `split` CTAs of a cluster
+// share a tile's depth when there are few tiles and add their accumulators
+// through each other's shared memory, in rank order.
+//
+// Warp 0 copies W, warp 1 copies X (as halves, made by halves_kernel), warp 2
+// multiplies, warp 3 holds the tensor memory, warps 4 to 11 convert and then store.
+constexpr int kStepDepth = 128;   // of a stage: 128 bytes of W, 256 of X
+template <int CTAS, int BN>
+struct Stream {
+  static constexpr int kChannels = 128 * CTAS;
+  static constexpr int kBytesW = 128 * kStepDepth, kHalfX = BN / CTAS * 128;
+  static constexpr int kBytesX = 2 * kHalfX, kStageBytes = kBytesW + kBytesX;
+  static constexpr bool kTwice = BN <= 64;   // two CTAs an SM
+  static constexpr int kStages = (kTwice ? 102400 : 196608) / kStageBytes;
+  static constexpr int kStagesA = kTwice ? 2 : 4;   // of halves in tensor memory
+  static constexpr int kColumnsA = kStepDepth / 2;
+  static constexpr int kColumns = kTwice ? 256 : 512;
+  static constexpr int kThreads = 384;
+  static constexpr int kSmem = kStages * kStageBytes + 1024;
+  static_assert(BN + kStagesA * kColumnsA <= kColumns, "tensor memory");
+  static_assert(BN * 128 * 4 <= kStages * kStageBytes, "the exchange of sums");
+};
+
+template <int CTAS, int BN>
+__global__ void __launch_bounds__(384, Stream<CTAS, BN>::kTwice ? 2 : 1)
+    gemmq_stream(const __grid_constant__ CUtensorMap map_w,
+                 const __grid_constant__ CUtensorMap map_x, GemmqAny a, int tiles_n, int steps,
+                 int split, int* status, int epoch, unsigned long long limit_ns,
+                 uint32_t extra_tx) {
+  using S = Stream<CTAS, BN>;
+  extern __shared__ uint8_t raw_smem[];
+  __shared__ alignas(8) uint64_t bar_words[4 * S::kStages + 2 * S::kStagesA + 1];
+  __shared__ uint32_t tmem_word;
+  __shared__ int dead_word;
+  volatile int* const dead = &dead_word;
+  const uint32_t ring = (smem_addr(raw_smem) + 1023u) & ~1023u;
+  const uint32_t w_full = smem_addr(bar_words), w_empty = w_full + 8 * S::kStages;
+  const uint32_t x_full = w_empty + 8 * S::kStages, x_empty = x_full + 8 * S::kStages;
+  const uint32_t a_full = x_empty + 8 * S::kStages, a_empty = a_full + 8 * S::kStagesA;
+  const uint32_t acc_full = a_empty + 8 * S::kStagesA;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int cluster = CTAS == 2 ? 2 : split;
+  const int rank = cluster > 1 ? (int)cluster_rank() : 0;
+  // tiles that share W side by side: it is read from HBM once
+  const int tile = blockIdx.x / cluster, tm = tile / tiles_n, tn = tile - tm * tiles_n;
+  // this CTA's channels and tokens, and its steps of the depth
+  const int row_w = tm * S::kChannels + (CTAS == 2 ? rank * 128 : 0);
+  const int row_x = tn * BN + (CTAS == 2 ? rank * (BN / CTAS) : 0);
+  const int part = CTAS == 2 ? 0 : rank;
+  const int s0 = (int)((long long)steps * part / split);
+  const int mine = (int)((long long)steps * (part + 1) / split) - s0;
+
+  // nothing before the kernel that makes X's halves is still running (it
+  // waits for its own predecessor before it lets this one start)
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S::kStages; ++s) {
+      mbar_init(w_full + 8 * s, 1);
+      mbar_init(w_empty + 8 * s, 8);
+      mbar_init(x_full + 8 * s, 1);
+      mbar_init(x_empty + 8 * s, 1);
+    }
+    for (int s = 0; s < S::kStagesA; ++s) {
+      mbar_init(a_full + 8 * s, 8 * CTAS);
+      mbar_init(a_empty + 8 * s, 1);
+    }
+    mbar_init(acc_full, 1);
+    dead_word = 0;
+    mbar_init_fence();
+  }
+  if (warp == 3) tmem_alloc<CTAS>(smem_addr(&tmem_word), S::kColumns);
+  tensor_fence_before();
+  __syncthreads();
+  if (CTAS == 2) cluster_sync();
+  tensor_fence_after();
+  const uint32_t tmem = tmem_word, tmem_a = tmem + BN;
+  const int group = (warp - 4) / 4, quarter = warp % 4;   // of warps 4 to 11
+  bool ok = true;
+
+  if (warp < 2 && lane == 0) {
+    // ---- copies of W (warp 0) or X (warp 1)
+    const uint32_t full = warp == 0 ? w_full : x_full, empty = warp == 0 ? w_empty : x_empty;
+    const uint32_t lead_full = CTAS == 2 && warp == 1 ? cluster_address(x_full, 0) : full;
+    if (warp == 1) asm volatile("griddepcontrol.wait;" ::: "memory");
+    int u = 0;
+    for (; u < mine; ++u) {
+      const int stage = u % S::kStages;
+      if (!wait_or_dead(empty + 8 * stage, (u / S::kStages & 1) ^ 1, dead, limit_ns)) break;
+      const uint32_t at = ring + stage * S::kStageBytes, bar = full + 8 * stage;
+      if (warp == 0) {
+        mbar_arrive_expect_tx(bar, S::kBytesW + extra_tx);
+        tensor_g2s<1>(at, &map_w, (s0 + u) * kStepDepth, row_w, bar);
+      } else {
+        if (CTAS == 1 || rank == 0) mbar_arrive_expect_tx(bar, CTAS * S::kBytesX + extra_tx);
+        const uint32_t lead = lead_full + 8 * stage;
+        tensor_g2s<CTAS>(at + S::kBytesW, &map_x, (s0 + u) * kStepDepth, row_x, lead);
+        tensor_g2s<CTAS>(at + S::kBytesW + S::kHalfX, &map_x, (s0 + u) * kStepDepth + kDepth, row_x,
+                         lead);
+      }
+    }
+    // the arrivals of the last products reach this CTA before it may exit
+    if (u == mine && warp == 1) {
+      for (int s = max(0, mine - S::kStages); ok && s < mine; ++s)
+        ok = wait_or_dead(x_empty + 8 * (s % S::kStages), s / S::kStages & 1, dead, limit_ns);
+      for (int s = max(0, mine - S::kStagesA); ok && s < mine; ++s)
+        ok = wait_or_dead(a_empty + 8 * (s % S::kStagesA), s / S::kStagesA & 1, dead, limit_ns);
+    }
+    if (u < mine) {
+      // given up: copies in flight land, or have had their time to
+      const unsigned long long t0 = global_ns();
+      for (int s = max(0, u - S::kStages); s < u; ++s)
+        while (!mbar_try_wait(full + 8 * (s % S::kStages), s / S::kStages & 1) &&
+               global_ns() - t0 <= limit_ns) {
+        }
+      ok = false;
+    }
+  } else if (warp == 2 && lane == 0 && (CTAS == 1 || rank == 0)) {
+    // ---- products
+    constexpr uint32_t idesc = half_mma(S::kChannels, BN);
+    for (int u = 0; u < mine; ++u) {
+      const int stage = u % S::kStages, sa = u % S::kStagesA;
+      if (!wait_or_dead(x_full + 8 * stage, u / S::kStages & 1, dead, limit_ns) ||
+          !wait_or_dead(a_full + 8 * sa, u / S::kStagesA & 1, dead, limit_ns)) {
+        ok = false;
+        break;
+      }
+      tensor_fence_after();
+      const uint32_t at = ring + stage * S::kStageBytes + S::kBytesW;
+#pragma unroll
+      for (int q = 0; q < kStepDepth / 16; ++q)
+        mma_half_tmem<CTAS>(tmem, tmem_a + sa * S::kColumnsA + 8 * q,
+                            tile_descriptor(at + q / 4 * S::kHalfX) + 2 * (q % 4), idesc,
+                            u > 0 || q > 0);
+      mma_commit<CTAS>(x_empty + 8 * stage);
+      mma_commit<CTAS>(a_empty + 8 * sa);
+    }
+    if (ok) mma_commit<CTAS>(acc_full);
+  } else if (warp >= 4) {
+    // ---- W to halves: a thread a channel, a group of four warps each half of the depth.
+    // Every warp takes every step: a parity wait that skipped a phase would match the
+    // one before it.
+    const int row = quarter * 32 + lane;
+    const uint32_t lead_full = CTAS == 2 ? cluster_address(a_full, 0) : a_full;
+    for (int u = 0; u < mine; ++u) {
+      const int stage = u % S::kStages, sa = u % S::kStagesA;
+      ok = wait_or_dead(w_full + 8 * stage, u / S::kStages & 1, dead, limit_ns);
+      if (!__all_sync(0xffffffffu, ok)) {
+        ok = false;
+        break;
+      }
+      const uint32_t at = ring + stage * S::kStageBytes + row * 128;
+      uint4 q[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) q[c] = lds128(at + (((4 * group + c) ^ (row & 7)) << 4));
+      __syncwarp();
+      if (lane == 0) mbar_arrive(w_empty + 8 * stage);
+      ok = wait_or_dead(a_empty + 8 * sa, (u / S::kStagesA & 1) ^ 1, dead, limit_ns);
+      if (!__all_sync(0xffffffffu, ok)) {
+        ok = false;
+        break;
+      }
+      tensor_fence_after();
+      const uint32_t to =
+          tmem_a + ((uint32_t)(quarter * 32) << 16) + sa * S::kColumnsA + group * 32;
+#pragma unroll
+      for (int c = 0; c < 4; c += 2) {
+        uint32_t h[16];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          halves_of(q[c + e].x, h[8 * e], h[8 * e + 1]);
+          halves_of(q[c + e].y, h[8 * e + 2], h[8 * e + 3]);
+          halves_of(q[c + e].z, h[8 * e + 4], h[8 * e + 5]);
+          halves_of(q[c + e].w, h[8 * e + 6], h[8 * e + 7]);
+        }
+        tmem_store16(to + 8 * c, h);
+      }
+      tmem_stored();
+      tensor_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (CTAS == 2)
+          mbar_arrive_cluster(lead_full + 8 * sa);
+        else
+          mbar_arrive(a_full + 8 * sa);
+      }
+    }
+    // ---- results: a warp of each group for every 32 lanes, 16 columns in turn
+    if (ok) ok = wait_or_dead(acc_full, 0, dead, limit_ns);
+    ok = __all_sync(0xffffffffu, ok);
+    tensor_fence_after();
+  }
+  // a warp's failure is the CTA's: its results are NaN
+  __syncwarp();
+  if (!ok) *dead = 1;
+  const long long i = (long long)row_w + quarter * 32 + lane;
+  const float nan = __uint_as_float(0x7fc00000u);
+  if (split == 1) {
+    __syncthreads();
+    const bool good = *dead == 0;
+    if (warp >= 4)
+      for (int c0 = group * 16; c0 < BN; c0 += 32) {
+        const long long j0 = (long long)tn * BN + c0;
+        if (j0 >= a.n) break;
+        uint32_t r[16];
+        tmem_load16(r, tmem + ((uint32_t)(quarter * 32) << 16) + c0);
+        if (i < a.m)
+#pragma unroll
+          for (int c = 0; c < 16; ++c)
+            if (j0 + c < a.n) store_any(a, i, j0 + c, good ? __uint_as_float(r[c]) : nan);
+      }
+    if (CTAS == 2) {
+      tensor_fence_before();
+      cluster_sync();
+      tensor_fence_after();
+    }
+  } else {
+    // CTA q of the cluster adds columns q*width .. of all: (rank, column, channel)
+    // in its shared memory, which every CTA has finished with
+    cluster_sync();
+    const int width = BN / split;
+    const bool good = *dead == 0;
+    if (warp >= 4)
+      for (int c0 = group * 16; c0 < BN; c0 += 32) {
+        uint32_t r[16];
+        tmem_load16(r, tmem + ((uint32_t)(quarter * 32) << 16) + c0);
+#pragma unroll
+        for (int c = 0; c < 16; ++c) {
+          const int owner = (c0 + c) / width, col = (c0 + c) - owner * width;
+          const uint32_t to = cluster_address(ring, owner) +
+                              ((rank * width + col) * 128 + quarter * 32 + lane) * 4;
+          asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to),
+                       "f"(good ? __uint_as_float(r[c]) : nan)
+                       : "memory");
+        }
+      }
+    cluster_sync();
+    if (warp >= 4)
+      for (int c = group; c < width; c += 2) {
+        const long long j = (long long)tn * BN + rank * width + c;
+        if (j >= a.n || i >= a.m) continue;
+        float v = 0.f;
+        for (int r = 0; r < split; ++r) {
+          float p;
+          asm volatile("ld.shared.f32 %0, [%1];"
+                       : "=f"(p)
+                       : "r"(ring + ((r * width + c) * 128 + quarter * 32 + lane) * 4)
+                       : "memory");
+          v += p;
+        }
+        store_any(a, i, j, v);
+      }
+  }
+  if (*dead != 0 && threadIdx.x == 0) atomicMax(status, epoch);
+  tensor_fence_before();
+  __syncthreads();
+  tensor_fence_after();
+  if (warp == 3) tmem_free<CTAS>(tmem, S::kColumns);
 }
 
 }  // namespace xsymv

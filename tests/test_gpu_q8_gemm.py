@@ -158,6 +158,35 @@ def test_repeats_bitwise_on_another_stream(n):
     assert all(torch.equal(outs[0], y) for y in outs[1:])
 
 
+@pytest.mark.parametrize("n", [1, 3, 8, 13, 30, 37, 64, 100, 200, 500, 1500])
+def test_many_calls_in_a_row(n):
+    """calls queued behind one another, different operands in turn, give what each
+    gives alone"""
+    m, k = 2048, 4096
+    g = gen(n)
+    sets = []
+    for _ in range(3):
+        w, x = integers(g, m, k), integers(g, n, k)
+        y = torch.empty((n, m), device="cuda")
+        sets.append((w, x, y))
+    alone = []
+    for w, x, y in sets:
+        assert xs.gemmq("s", m, n, k, 1.0, w, k, None, x, k, None, 0.0, y, m) == 0
+        torch.cuda.synchronize()
+        want = x.double() @ w.double().T
+        assert torch.equal(y.double(), want)
+        alone.append(y.clone())
+    for _ in range(40):
+        for w, x, y in sets:
+            y.fill_(float("nan"))
+        for _ in range(3):
+            for w, x, y in sets:
+                assert xs.gemmq("s", m, n, k, 1.0, w, k, None, x, k, None, 0.0, y, m) == 0
+        for (w, x, y), a in zip(sets, alone):
+            assert torch.equal(y, a)
+    assert xs.xsymv_sync_status() == 0
+
+
 @pytest.mark.parametrize("n", [2, 40])
 def test_offsets_beyond_32_bits(n):
     """channels, tokens and outputs so far apart that offsets pass 2^32 bytes"""
