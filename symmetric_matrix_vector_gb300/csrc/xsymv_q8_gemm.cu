@@ -151,42 +151,66 @@ int* status_word(cudaStream_t st, int* status, int* epoch) {
   return static_cast<int*>(workspace(256, st, status, 0, epoch));
 }
 
+cudaError_t launch_align(int rows, int k, const int8_t* q, long long ldq, int8_t* out,
+                         long long ldo, cudaStream_t st) {
+  const dim3 block = pack_block(ldo / kPack);
+  return launch_after(align_kernel, pack_grid(rows, ldo / kPack, block), block, 0, st, rows, k, q,
+                      ldq, out, ldo);
+}
+
 template <int CTAS, int BN>
 int gemmq_streamed(const GemmqAny& a, int sms, cudaStream_t st) {
   using S = Stream<CTAS, BN>;
   const int steps = (int)((a.k + (long long)kStepDepth - 1) / kStepDepth);
-  const long long kp = (long long)steps * kStepDepth;
-  const bool on_grid = reinterpret_cast<uintptr_t>(a.W) % 16 == 0 && a.ldw % 16 == 0;
-  const long long ldo = (a.k + 15LL) / 16 * 16;
+  const long long kp = (long long)steps * kStepDepth, ldo = (a.k + 15LL) / 16 * 16;
+  // tensor copies need 16-byte boundaries: what is not on them is copied first
+  auto on_grid = [](const int8_t* p, long long ld) {
+    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % 16 == 0;
+  };
+  const bool move_w = !on_grid(a.W, a.ldw), move_x = S::kRaw && !on_grid(a.X, a.ldx);
   Pieces pieces;
-  const size_t at_x = pieces.add((size_t)a.n * kp * 2);
-  const size_t at_w = on_grid ? 0 : pieces.add((size_t)a.m * ldo);
-  int status = XSYMV_OK, epoch = 0;
+  const size_t at_w = move_w ? pieces.add((size_t)a.m * ldo) : 0;
+  const size_t at_x = S::kRaw ? (move_x ? pieces.add((size_t)a.n * ldo) : 0)
+                              : pieces.add((size_t)a.n * kp * 2);
+  int status = XSYMV_OK, epoch = 0, kernels = 1;
   int* const word = status_word(st, &status, &epoch);
   if (word == nullptr) return status;
-  char* ws = static_cast<char*>(workspace(pieces.bytes, st, &status, kSlotOperands, nullptr));
-  if (ws == nullptr) return status;
-  __half* const x = reinterpret_cast<__half*>(ws + at_x);
-  const int8_t* const w = on_grid ? a.W : reinterpret_cast<int8_t*>(ws + at_w);
-  CUtensorMap map_w, map_x;
-  if (!map_rows(&map_w, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, w, a.k, a.m, on_grid ? a.ldw : ldo, 128) ||
-      !map_halves(&map_x, x, kp, a.n, BN / CTAS))
-    return XSYMV_ERR_CUDA;
-  int kernels = 2;
+  char* ws = nullptr;
+  if (pieces.bytes > 0) {
+    ws = static_cast<char*>(workspace(pieces.bytes, st, &status, kSlotOperands, nullptr));
+    if (ws == nullptr) return status;
+  }
+  const int8_t* w = a.W;
+  const int8_t* x = a.X;
+  long long ldw = a.ldw, ldx = a.ldx;
   cudaError_t e = cudaSuccess;
-  if (!on_grid) {
-    const dim3 block = pack_block(ldo / kPack);
-    e = launch_after(align_kernel, pack_grid(a.m, ldo / kPack, block), block, 0, st, a.m, a.k, a.W,
-                     a.ldw, reinterpret_cast<int8_t*>(ws + at_w), ldo);
+  if (move_w) {
+    int8_t* to = reinterpret_cast<int8_t*>(ws + at_w);
+    e = launch_align(a.m, a.k, a.W, a.ldw, to, ldo, st);
+    w = to, ldw = ldo, ++kernels;
+  }
+  if (e == cudaSuccess && move_x) {
+    int8_t* to = reinterpret_cast<int8_t*>(ws + at_x);
+    e = launch_align(a.n, a.k, a.X, a.ldx, to, ldo, st);
+    x = to, ldx = ldo, ++kernels;
+  }
+  CUtensorMap map_w, map_x;
+  bool mapped = map_rows(&map_w, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, w, a.k, a.m, ldw, 128);
+  if (S::kRaw) {
+    mapped = mapped && map_rows(&map_x, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, x, a.k, a.n, ldx, BN);
+  } else {
+    __half* to = reinterpret_cast<__half*>(ws + at_x);
+    if (e == cudaSuccess) e = launch_halves(a.n, a.k, (int)kp, a.X, a.ldx, to, st);
+    mapped = mapped && map_halves(&map_x, to, kp, a.n, BN / CTAS);
     ++kernels;
   }
-  if (e == cudaSuccess) e = launch_halves(a.n, a.k, (int)kp, a.X, a.ldx, x, st);
+  if (!mapped) return XSYMV_ERR_CUDA;
   if (e == cudaSuccess) {
     const long long tiles_m = (a.m + S::kChannels - 1LL) / S::kChannels;
     const long long tiles_n = (a.n + BN - 1LL) / BN;
     int split = 1;
     while (CTAS == 1 && split < 8 && split * 2 <= steps &&
-           tiles_m * tiles_n * split * 2 <= (S::kTwice ? 2LL : 1LL) * sms)
+           tiles_m * tiles_n * split * 2 <= (S::kRaw ? 2LL : 1LL) * sms)
       split *= 2;
     const int cluster = CTAS == 2 ? 2 : split;
     e = launch_cluster(gemmq_stream<CTAS, BN>, (unsigned)(tiles_m * tiles_n * cluster), cluster,

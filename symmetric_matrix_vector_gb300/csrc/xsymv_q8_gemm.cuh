@@ -508,6 +508,7 @@ __global__ void __launch_bounds__(192, 1)
                            ok ? __uint_as_float(r[c]) : __uint_as_float(0x7fc00000u), channel,
                            token_scale[set][c0 + c]);
         }
+        __syncwarp();
       }
       tensor_fence_before();
       __syncwarp();
@@ -537,41 +538,76 @@ __global__ void __launch_bounds__(192, 1)
 // share a tile's depth when there are few tiles and add their accumulators
 // through each other's shared memory, in rank order.
 //
-// Warp 0 copies W, warp 1 copies X (as halves, made by halves_kernel), warp 2
-// multiplies, warp 3 holds the tensor memory, warps 4 to 11 convert and then store.
-constexpr int kStepDepth = 128;   // of a stage: 128 bytes of W, 256 of X
+// Up to 64 tokens X too arrives as 8-bit integers and four more warps make its
+// halves in shared memory (RAW): the call is one kernel.  Wider tiles read halves
+// that halves_kernel made: made here they would cost shared memory twice the traffic.
+//
+// Warp 0 copies W, warp 1 copies X, warp 2 multiplies, warp 3 holds the tensor memory,
+// warps 4 to 11 convert W and store the results, warps 12 to 15 (RAW) convert X.
+constexpr int kStepDepth = 128;   // of a step: 128 bytes of W, 256 of X's halves
 template <int CTAS, int BN>
 struct Stream {
+  static constexpr bool kRaw = BN <= 64;   // and two CTAs an SM
   static constexpr int kChannels = 128 * CTAS;
   static constexpr int kBytesW = 128 * kStepDepth, kHalfX = BN / CTAS * 128;
-  static constexpr int kBytesX = 2 * kHalfX, kStageBytes = kBytesW + kBytesX;
-  static constexpr bool kTwice = BN <= 64;   // two CTAs an SM
-  static constexpr int kStages = (kTwice ? 102400 : 196608) / kStageBytes;
-  static constexpr int kStagesA = kTwice ? 2 : 4;   // of halves in tensor memory
+  static constexpr int kBytesX = 2 * kHalfX, kBytesRaw = kRaw ? BN * kStepDepth : 0;
+  // steps of W, of X's halves and of W's halves in tensor memory, of raw X
+  static constexpr int kStagesA = kRaw ? 2 : 4, kStagesX = kStagesA, kStagesRaw = kRaw ? 2 : 0;
+  static constexpr int kStagesW = kRaw ? (BN == 64 ? 3 : 5) : 4;
   static constexpr int kColumnsA = kStepDepth / 2;
-  static constexpr int kColumns = kTwice ? 256 : 512;
-  static constexpr int kThreads = 384;
-  static constexpr int kSmem = kStages * kStageBytes + 1024;
+  static constexpr int kColumns = kRaw ? 256 : 512;
+  static constexpr int kThreads = kRaw ? 512 : 384;
+  static constexpr int kAtX = kStagesW * kBytesW, kAtRaw = kAtX + kStagesX * kBytesX;
+  static constexpr int kRing = kAtRaw + kStagesRaw * kBytesRaw;
+  static constexpr int kSmem = kRing + 1024;
   static_assert(BN + kStagesA * kColumnsA <= kColumns, "tensor memory");
-  static_assert(BN * 128 * 4 <= kStages * kStageBytes, "the exchange of sums");
+  static_assert(BN * 128 * 4 <= kRing, "the exchange of sums");
 };
 
+// v[c] * channel * token[c] + beta * y[c] to `count` of 16 tokens of a channel
+template <class T>
+__device__ __forceinline__ void store_tokens(T* y, long long ldy, int count, const float (&v)[16],
+                                             float channel, const float* token, float beta) {
+#pragma unroll
+  for (int c = 0; c < 16; ++c)
+    if (c < count) {
+      float r = v[c] * channel * token[c];
+      if (beta != 0.f) r = fmaf(beta, to_float(y[c * ldy]), r);
+      y[c * ldy] = from_float<T>(r);
+    }
+}
+__device__ __forceinline__ void store_tokens_any(const GemmqAny& a, long long i, long long j,
+                                                 int count, const float (&v)[16], float channel,
+                                                 const float* token) {
+  const long long at = j * a.ldy + i;
+  if (a.type == 's')
+    store_tokens(static_cast<float*>(a.Y) + at, a.ldy, count, v, channel, token, a.beta);
+  else if (a.type == 'h')
+    store_tokens(static_cast<__half*>(a.Y) + at, a.ldy, count, v, channel, token, a.beta);
+  else
+    store_tokens(static_cast<__nv_bfloat16*>(a.Y) + at, a.ldy, count, v, channel, token, a.beta);
+}
+
 template <int CTAS, int BN>
-__global__ void __launch_bounds__(384, Stream<CTAS, BN>::kTwice ? 2 : 1)
+__global__ void __launch_bounds__(Stream<CTAS, BN>::kThreads, Stream<CTAS, BN>::kRaw ? 2 : 1)
     gemmq_stream(const __grid_constant__ CUtensorMap map_w,
                  const __grid_constant__ CUtensorMap map_x, GemmqAny a, int tiles_n, int steps,
                  int split, int* status, int epoch, unsigned long long limit_ns,
                  uint32_t extra_tx) {
   using S = Stream<CTAS, BN>;
+  constexpr bool RAW = S::kRaw;
+  // the ring that X's copies fill: raw X, or its halves
+  constexpr int COPIES = RAW ? S::kStagesRaw : S::kStagesX;
   extern __shared__ uint8_t raw_smem[];
-  __shared__ alignas(8) uint64_t bar_words[4 * S::kStages + 2 * S::kStagesA + 1];
+  __shared__ alignas(8) uint64_t bar_words[2 * S::kStagesW + 2 * COPIES + 2 * S::kStagesA + 1];
   __shared__ uint32_t tmem_word;
   __shared__ int dead_word;
+  __shared__ float token_scale[BN];
   volatile int* const dead = &dead_word;
   const uint32_t ring = (smem_addr(raw_smem) + 1023u) & ~1023u;
-  const uint32_t w_full = smem_addr(bar_words), w_empty = w_full + 8 * S::kStages;
-  const uint32_t x_full = w_empty + 8 * S::kStages, x_empty = x_full + 8 * S::kStages;
-  const uint32_t a_full = x_empty + 8 * S::kStages, a_empty = a_full + 8 * S::kStagesA;
+  const uint32_t w_full = smem_addr(bar_words), w_empty = w_full + 8 * S::kStagesW;
+  const uint32_t x_full = w_empty + 8 * S::kStagesW, x_empty = x_full + 8 * COPIES;
+  const uint32_t a_full = x_empty + 8 * COPIES, a_empty = a_full + 8 * S::kStagesA;
   const uint32_t acc_full = a_empty + 8 * S::kStagesA;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int cluster = CTAS == 2 ? 2 : split;
@@ -585,18 +621,21 @@ __global__ void __launch_bounds__(384, Stream<CTAS, BN>::kTwice ? 2 : 1)
   const int s0 = (int)((long long)steps * part / split);
   const int mine = (int)((long long)steps * (part + 1) / split) - s0;
 
-  // nothing before the kernel that makes X's halves is still running (it
-  // waits for its own predecessor before it lets this one start)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (threadIdx.x == 0) {
-    for (int s = 0; s < S::kStages; ++s) {
+    // the first steps of W on their way to L2 while the predecessor still runs
+    for (int u = 0; u < min(mine, 8); ++u)
+      tensor_prefetch(&map_w, (s0 + u) * kStepDepth, row_w);
+    for (int s = 0; s < S::kStagesW; ++s) {
       mbar_init(w_full + 8 * s, 1);
       mbar_init(w_empty + 8 * s, 8);
+    }
+    for (int s = 0; s < COPIES; ++s) {
       mbar_init(x_full + 8 * s, 1);
-      mbar_init(x_empty + 8 * s, 1);
+      mbar_init(x_empty + 8 * s, RAW ? 4 : 1);
     }
     for (int s = 0; s < S::kStagesA; ++s) {
-      mbar_init(a_full + 8 * s, 8 * CTAS);
+      mbar_init(a_full + 8 * s, (RAW ? 12 : 8) * CTAS);
       mbar_init(a_empty + 8 * s, 1);
     }
     mbar_init(acc_full, 1);
@@ -608,43 +647,50 @@ __global__ void __launch_bounds__(384, Stream<CTAS, BN>::kTwice ? 2 : 1)
   __syncthreads();
   if (CTAS == 2) cluster_sync();
   tensor_fence_after();
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const uint32_t tmem = tmem_word, tmem_a = tmem + BN;
   const int group = (warp - 4) / 4, quarter = warp % 4;   // of warps 4 to 11
+  const long long i = (long long)row_w + quarter * 32 + lane;   // this thread's channel
+  const long long j0 = (long long)tn * BN;
+  float channel = 0.f;
   bool ok = true;
 
   if (warp < 2 && lane == 0) {
     // ---- copies of W (warp 0) or X (warp 1)
-    const uint32_t full = warp == 0 ? w_full : x_full, empty = warp == 0 ? w_empty : x_empty;
-    const uint32_t lead_full = CTAS == 2 && warp == 1 ? cluster_address(x_full, 0) : full;
-    if (warp == 1) asm volatile("griddepcontrol.wait;" ::: "memory");
+    const bool w = warp == 0;
+    const int stages = w ? S::kStagesW : COPIES;
+    const uint32_t full = w ? w_full : x_full, empty = w ? w_empty : x_empty;
+    const uint32_t lead_full = CTAS == 2 && !w ? cluster_address(x_full, 0) : full;
     int u = 0;
     for (; u < mine; ++u) {
-      const int stage = u % S::kStages;
-      if (!wait_or_dead(empty + 8 * stage, (u / S::kStages & 1) ^ 1, dead, limit_ns)) break;
-      const uint32_t at = ring + stage * S::kStageBytes, bar = full + 8 * stage;
-      if (warp == 0) {
+      const int stage = u % stages, depth = (s0 + u) * kStepDepth;
+      if (!wait_or_dead(empty + 8 * stage, (u / stages & 1) ^ 1, dead, limit_ns)) break;
+      const uint32_t bar = full + 8 * stage;
+      if (w) {
         mbar_arrive_expect_tx(bar, S::kBytesW + extra_tx);
-        tensor_g2s<1>(at, &map_w, (s0 + u) * kStepDepth, row_w, bar);
+        tensor_g2s<1>(ring + stage * S::kBytesW, &map_w, depth, row_w, bar);
+      } else if (RAW) {
+        mbar_arrive_expect_tx(bar, S::kBytesRaw + extra_tx);
+        tensor_g2s<1>(ring + S::kAtRaw + stage * S::kBytesRaw, &map_x, depth, row_x, bar);
       } else {
         if (CTAS == 1 || rank == 0) mbar_arrive_expect_tx(bar, CTAS * S::kBytesX + extra_tx);
-        const uint32_t lead = lead_full + 8 * stage;
-        tensor_g2s<CTAS>(at + S::kBytesW, &map_x, (s0 + u) * kStepDepth, row_x, lead);
-        tensor_g2s<CTAS>(at + S::kBytesW + S::kHalfX, &map_x, (s0 + u) * kStepDepth + kDepth, row_x,
-                         lead);
+        const uint32_t lead = lead_full + 8 * stage, at = ring + S::kAtX + stage * S::kBytesX;
+        tensor_g2s<CTAS>(at, &map_x, depth, row_x, lead);
+        tensor_g2s<CTAS>(at + S::kHalfX, &map_x, depth + kDepth, row_x, lead);
       }
     }
     // the arrivals of the last products reach this CTA before it may exit
-    if (u == mine && warp == 1) {
-      for (int s = max(0, mine - S::kStages); ok && s < mine; ++s)
-        ok = wait_or_dead(x_empty + 8 * (s % S::kStages), s / S::kStages & 1, dead, limit_ns);
+    if (u == mine && !w) {
+      for (int s = max(0, mine - COPIES); ok && s < mine; ++s)
+        ok = wait_or_dead(x_empty + 8 * (s % COPIES), s / COPIES & 1, dead, limit_ns);
       for (int s = max(0, mine - S::kStagesA); ok && s < mine; ++s)
         ok = wait_or_dead(a_empty + 8 * (s % S::kStagesA), s / S::kStagesA & 1, dead, limit_ns);
     }
     if (u < mine) {
       // given up: copies in flight land, or have had their time to
       const unsigned long long t0 = global_ns();
-      for (int s = max(0, u - S::kStages); s < u; ++s)
-        while (!mbar_try_wait(full + 8 * (s % S::kStages), s / S::kStages & 1) &&
+      for (int s = max(0, u - stages); s < u; ++s)
+        while (!mbar_try_wait(full + 8 * (s % stages), s / stages & 1) &&
                global_ns() - t0 <= limit_ns) {
         }
       ok = false;
@@ -653,41 +699,40 @@ __global__ void __launch_bounds__(384, Stream<CTAS, BN>::kTwice ? 2 : 1)
     // ---- products
     constexpr uint32_t idesc = half_mma(S::kChannels, BN);
     for (int u = 0; u < mine; ++u) {
-      const int stage = u % S::kStages, sa = u % S::kStagesA;
-      if (!wait_or_dead(x_full + 8 * stage, u / S::kStages & 1, dead, limit_ns) ||
-          !wait_or_dead(a_full + 8 * sa, u / S::kStagesA & 1, dead, limit_ns)) {
-        ok = false;
-        break;
-      }
+      const int sx = u % S::kStagesX, sa = u % S::kStagesA;
+      if (!RAW) ok = wait_or_dead(x_full + 8 * sx, u / S::kStagesX & 1, dead, limit_ns);
+      if (ok) ok = wait_or_dead(a_full + 8 * sa, u / S::kStagesA & 1, dead, limit_ns);
+      if (!ok) break;
       tensor_fence_after();
-      const uint32_t at = ring + stage * S::kStageBytes + S::kBytesW;
+      const uint32_t at = ring + S::kAtX + sx * S::kBytesX;
 #pragma unroll
       for (int q = 0; q < kStepDepth / 16; ++q)
         mma_half_tmem<CTAS>(tmem, tmem_a + sa * S::kColumnsA + 8 * q,
                             tile_descriptor(at + q / 4 * S::kHalfX) + 2 * (q % 4), idesc,
                             u > 0 || q > 0);
-      mma_commit<CTAS>(x_empty + 8 * stage);
+      if (!RAW) mma_commit<CTAS>(x_empty + 8 * sx);
       mma_commit<CTAS>(a_empty + 8 * sa);
     }
     if (ok) mma_commit<CTAS>(acc_full);
-  } else if (warp >= 4) {
+  } else if (warp >= 4 && warp < 12) {
     // ---- W to halves: a thread a channel, a group of four warps each half of the depth.
     // Every warp takes every step: a parity wait that skipped a phase would match the
     // one before it.
     const int row = quarter * 32 + lane;
     const uint32_t lead_full = CTAS == 2 ? cluster_address(a_full, 0) : a_full;
+    if (i < a.m) channel = a.sw != nullptr ? a.sw[i] : 1.f;
     for (int u = 0; u < mine; ++u) {
-      const int stage = u % S::kStages, sa = u % S::kStagesA;
-      ok = wait_or_dead(w_full + 8 * stage, u / S::kStages & 1, dead, limit_ns);
+      const int stage = u % S::kStagesW, sa = u % S::kStagesA;
+      ok = wait_or_dead(w_full + 8 * stage, u / S::kStagesW & 1, dead, limit_ns);
       if (!__all_sync(0xffffffffu, ok)) {
         ok = false;
         break;
       }
-      const uint32_t at = ring + stage * S::kStageBytes + row * 128;
+      const uint32_t at = ring + stage * S::kBytesW + row * 128;
       uint4 q[4];
 #pragma unroll
       for (int c = 0; c < 4; ++c) q[c] = lds128(at + (((4 * group + c) ^ (row & 7)) << 4));
-      __syncwarp();
+      reads_done();
       if (lane == 0) mbar_arrive(w_empty + 8 * stage);
       ok = wait_or_dead(a_empty + 8 * sa, (u / S::kStagesA & 1) ^ 1, dead, limit_ns);
       if (!__all_sync(0xffffffffu, ok)) {
@@ -719,42 +764,85 @@ __global__ void __launch_bounds__(384, Stream<CTAS, BN>::kTwice ? 2 : 1)
           mbar_arrive(a_full + 8 * sa);
       }
     }
-    // ---- results: a warp of each group for every 32 lanes, 16 columns in turn
+    // the accumulators, complete
     if (ok) ok = wait_or_dead(acc_full, 0, dead, limit_ns);
     ok = __all_sync(0xffffffffu, ok);
-    tensor_fence_after();
+  } else if (RAW && warp >= 12) {
+    // ---- X to halves: 16 elements a thread in turn, 8 threads a token
+    const int id = (int)threadIdx.x - 384;
+    for (int u = 0; u < mine; ++u) {
+      const int stage = u % COPIES, sa = u % S::kStagesA;
+      ok = wait_or_dead(x_full + 8 * stage, u / COPIES & 1, dead, limit_ns);
+      if (!__all_sync(0xffffffffu, ok)) {
+        ok = false;
+        break;
+      }
+      uint4 q[BN / 16];
+#pragma unroll
+      for (int e = 0; e < BN / 16; ++e) {
+        const int r = id / 8 + 16 * e, c = id % 8;
+        q[e] = lds128(ring + S::kAtRaw + stage * S::kBytesRaw + r * 128 + ((c ^ (r & 7)) << 4));
+      }
+      reads_done();
+      if (lane == 0) mbar_arrive(x_empty + 8 * stage);
+      ok = wait_or_dead(a_empty + 8 * sa, (u / S::kStagesA & 1) ^ 1, dead, limit_ns);
+      if (!__all_sync(0xffffffffu, ok)) {
+        ok = false;
+        break;
+      }
+#pragma unroll
+      for (int e = 0; e < BN / 16; ++e) {
+        const int r = id / 8 + 16 * e, c = id % 8;
+        const uint32_t to = ring + S::kAtX + sa * S::kBytesX + c / 4 * S::kHalfX + r * 128;
+        uint32_t h[8];
+        halves_of(q[e].x, h[0], h[1]);
+        halves_of(q[e].y, h[2], h[3]);
+        halves_of(q[e].z, h[4], h[5]);
+        halves_of(q[e].w, h[6], h[7]);
+        sts128(to + (((c % 4 * 2) ^ (r & 7)) << 4), h[0], h[1], h[2], h[3]);
+        sts128(to + (((c % 4 * 2 + 1) ^ (r & 7)) << 4), h[4], h[5], h[6], h[7]);
+      }
+      // what the tensor cores read, which see shared memory as copies do
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) mbar_arrive(a_full + 8 * sa);
+    }
+  } else if (warp == 3) {
+    for (int c = lane; c < BN; c += 32)
+      token_scale[c] = j0 + c < a.n ? token_factor(a, j0 + c) : 0.f;
   }
   // a warp's failure is the CTA's: its results are NaN
   __syncwarp();
   if (!ok) *dead = 1;
-  const long long i = (long long)row_w + quarter * 32 + lane;
   const float nan = __uint_as_float(0x7fc00000u);
   if (split == 1) {
     __syncthreads();
+    tensor_fence_after();
     const bool good = *dead == 0;
-    if (warp >= 4)
-      for (int c0 = group * 16; c0 < BN; c0 += 32) {
-        const long long j0 = (long long)tn * BN + c0;
-        if (j0 >= a.n) break;
+    if (warp >= 4 && warp < 12)
+      for (int c0 = group * 16; c0 < BN && j0 + c0 < a.n; c0 += 32) {
         uint32_t r[16];
         tmem_load16(r, tmem + ((uint32_t)(quarter * 32) << 16) + c0);
-        if (i < a.m)
+        float v[16];
 #pragma unroll
-          for (int c = 0; c < 16; ++c)
-            if (j0 + c < a.n) store_any(a, i, j0 + c, good ? __uint_as_float(r[c]) : nan);
+        for (int c = 0; c < 16; ++c) v[c] = good ? __uint_as_float(r[c]) : nan;
+        if (i < a.m)
+          store_tokens_any(a, i, j0 + c0, (int)min(16LL, a.n - j0 - c0), v, channel,
+                           token_scale + c0);
+        __syncwarp();
       }
     if (CTAS == 2) {
       tensor_fence_before();
       cluster_sync();
-      tensor_fence_after();
     }
   } else {
     // CTA q of the cluster adds columns q*width .. of all: (rank, column, channel)
     // in its shared memory, which every CTA has finished with
     cluster_sync();
+    tensor_fence_after();
     const int width = BN / split;
     const bool good = *dead == 0;
-    if (warp >= 4)
+    if (warp >= 4 && warp < 12)
       for (int c0 = group * 16; c0 < BN; c0 += 32) {
         uint32_t r[16];
         tmem_load16(r, tmem + ((uint32_t)(quarter * 32) << 16) + c0);
@@ -769,23 +857,26 @@ __global__ void __launch_bounds__(384, Stream<CTAS, BN>::kTwice ? 2 : 1)
         }
       }
     cluster_sync();
-    if (warp >= 4)
+    if (warp >= 4 && warp < 12)
       for (int c = group; c < width; c += 2) {
-        const long long j = (long long)tn * BN + rank * width + c;
-        if (j >= a.n || i >= a.m) continue;
-        float v = 0.f;
+        const int col = rank * width + c;
+        float sum = 0.f;
         for (int r = 0; r < split; ++r) {
           float p;
           asm volatile("ld.shared.f32 %0, [%1];"
                        : "=f"(p)
                        : "r"(ring + ((r * width + c) * 128 + quarter * 32 + lane) * 4)
                        : "memory");
-          v += p;
+          sum += p;
         }
-        store_any(a, i, j, v);
+        if (j0 + col < a.n && i < a.m) {
+          const float v[16] = {sum};
+          store_tokens_any(a, i, j0 + col, 1, v, channel, token_scale + col);
+        }
       }
   }
   if (*dead != 0 && threadIdx.x == 0) atomicMax(status, epoch);
+  __syncwarp();
   tensor_fence_before();
   __syncthreads();
   tensor_fence_after();

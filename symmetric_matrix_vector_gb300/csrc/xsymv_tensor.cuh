@@ -36,6 +36,14 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
+// All lanes' reads of shared memory so far have returned.  Without the fence an
+// arrival that hands the memory back to a copy can overtake loads on their way
+// (seen: a row, or 32, of the tile after next, once in some hundred calls).
+__device__ __forceinline__ void reads_done() {
+  __threadfence_block();
+  __syncwarp();
+}
+
 // Wait for phase `parity`, giving up once `limit_ns` have passed or another
 // wait of this CTA has given up (*dead).  A wait that gives up sets *dead.
 __device__ __forceinline__ bool wait_or_dead(uint32_t bar, uint32_t parity, volatile int* dead,
@@ -74,6 +82,19 @@ __device__ __forceinline__ void tensor_g2s(uint32_t dst, const CUtensorMap* map,
         " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
         "l"(map), "r"(x), "r"(y), "r"(bar)
         : "memory");
+}
+
+// the same box to L2
+__device__ __forceinline__ void tensor_prefetch(const CUtensorMap* map, int x, int y) {
+  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(map), "r"(x),
+               "r"(y)
+               : "memory");
+}
+__device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c,
+                                       uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c),
+               "r"(d)
+               : "memory");
 }
 
 // ----------------------------------------------------------- tensor cores --
