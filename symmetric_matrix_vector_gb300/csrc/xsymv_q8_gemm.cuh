@@ -450,34 +450,34 @@ __global__ void __launch_bounds__(192, 1)
         }
     }
     if (!ok || *dead != 0) atomicMax(status, epoch);
-  } else if (warp == 1 && lane == 0 && rank == 0) {
+  } else if (warp == 1 && rank == 0) {
     // ---- products
     constexpr uint32_t idesc = half_mma(S::kChannels, BN);
+    const uint32_t one = elect_one();
     int stage = 0, set = 0;
     uint32_t phase = 0, set_phase = 0;
     bool ok = true;
     for (int t = first_tile; ok && t < order.tiles; t += stride) {
-      if (!wait_or_dead(acc_empty + 8 * set, set_phase ^ 1, dead, limit_ns)) break;
+      ok = __all_sync(0xffffffffu, wait_or_dead(acc_empty + 8 * set, set_phase ^ 1, dead, limit_ns));
+      if (!ok) break;
       tensor_fence_after();
       for (int s = 0; s < steps; ++s) {
-        if (!wait_or_dead(full + 8 * stage, phase, dead, limit_ns)) {
-          ok = false;
-          break;
-        }
+        ok = __all_sync(0xffffffffu, wait_or_dead(full + 8 * stage, phase, dead, limit_ns));
+        if (!ok) break;
         tensor_fence_after();
         const uint32_t at = tiles_smem + stage * S::kStageBytes;
         const uint64_t dw = tile_descriptor(at), dx = tile_descriptor(at + S::kBytesW);
 #pragma unroll
         for (int q = 0; q < kDepth / 16; ++q)   // 16 halves: 32 bytes, 2 units of the descriptor
-          mma_half<CTAS>(tmem + set * BN, dw + 2 * q, dx + 2 * q, idesc, s > 0 || q > 0);
-        mma_commit<CTAS>(empty + 8 * stage);
+          mma_half<CTAS>(tmem + set * BN, dw + 2 * q, dx + 2 * q, idesc, s > 0 || q > 0, one);
+        mma_commit<CTAS>(empty + 8 * stage, one);
         if (++stage == S::kStages) stage = 0, phase ^= 1;
       }
-      if (ok) mma_commit<CTAS>(acc_full + 8 * set);
+      if (ok) mma_commit<CTAS>(acc_full + 8 * set, one);
       set ^= 1;
       if (set == 0) set_phase ^= 1;
     }
-    if (*dead != 0) atomicMax(status, epoch);
+    if (*dead != 0 && lane == 0) atomicMax(status, epoch);
   } else if (warp >= 2) {
     // ---- results: a warp may read the 32 lanes of tensor memory of its number mod 4
     const int quarter = warp % 4;
@@ -695,25 +695,28 @@ __global__ void __launch_bounds__(Stream<CTAS, BN>::kThreads, Stream<CTAS, BN>::
         }
       ok = false;
     }
-  } else if (warp == 2 && lane == 0 && (CTAS == 1 || rank == 0)) {
+  } else if (warp == 2 && (CTAS == 1 || rank == 0)) {
     // ---- products
     constexpr uint32_t idesc = half_mma(S::kChannels, BN);
+    const uint32_t one = elect_one();
     for (int u = 0; u < mine; ++u) {
       const int sx = u % S::kStagesX, sa = u % S::kStagesA;
       if (!RAW) ok = wait_or_dead(x_full + 8 * sx, u / S::kStagesX & 1, dead, limit_ns);
       if (ok) ok = wait_or_dead(a_full + 8 * sa, u / S::kStagesA & 1, dead, limit_ns);
+      ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       tensor_fence_after();
       const uint32_t at = ring + S::kAtX + sx * S::kBytesX;
+      const uint64_t lo = tile_descriptor(at), hi = tile_descriptor(at + S::kHalfX);
+      const uint32_t ta = tmem_a + sa * S::kColumnsA;
 #pragma unroll
       for (int q = 0; q < kStepDepth / 16; ++q)
-        mma_half_tmem<CTAS>(tmem, tmem_a + sa * S::kColumnsA + 8 * q,
-                            tile_descriptor(at + q / 4 * S::kHalfX) + 2 * (q % 4), idesc,
-                            u > 0 || q > 0);
-      if (!RAW) mma_commit<CTAS>(x_empty + 8 * sx);
-      mma_commit<CTAS>(a_empty + 8 * sa);
+        mma_half_tmem<CTAS>(tmem, ta + 8 * q, (q < 4 ? lo : hi) + 2 * (q % 4), idesc,
+                            u > 0 || q > 0, one);
+      if (!RAW) mma_commit<CTAS>(x_empty + 8 * sx, one);
+      mma_commit<CTAS>(a_empty + 8 * sa, one);
     }
-    if (ok) mma_commit<CTAS>(acc_full);
+    if (ok) mma_commit<CTAS>(acc_full, one);
   } else if (warp >= 4 && warp < 12) {
     // ---- W to halves: a thread a channel, a group of four warps each half of the depth.
     // Every warp takes every step: a parity wait that skipped a phase would match the
@@ -836,43 +839,54 @@ __global__ void __launch_bounds__(Stream<CTAS, BN>::kThreads, Stream<CTAS, BN>::
       cluster_sync();
     }
   } else {
-    // CTA q of the cluster adds columns q*width .. of all: (rank, column, channel)
+    // CTA q of the cluster adds columns q*width .. of all: [rank][column / 4][channel][column % 4]
     // in its shared memory, which every CTA has finished with
     cluster_sync();
     tensor_fence_after();
-    const int width = BN / split;
+    const int width = BN / split, chunk = min(width, 4);   // 2, 4 or more
     const bool good = *dead == 0;
     if (warp >= 4 && warp < 12)
       for (int c0 = group * 16; c0 < BN; c0 += 32) {
         uint32_t r[16];
         tmem_load16(r, tmem + ((uint32_t)(quarter * 32) << 16) + c0);
+        if (!good)
 #pragma unroll
-        for (int c = 0; c < 16; ++c) {
+          for (int c = 0; c < 16; ++c) r[c] = 0x7fc00000u;
+#pragma unroll
+        for (int c = 0; c < 16; c += 4) {
           const int owner = (c0 + c) / width, col = (c0 + c) - owner * width;
-          const uint32_t to = cluster_address(ring, owner) +
-                              ((rank * width + col) * 128 + quarter * 32 + lane) * 4;
-          asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to),
-                       "f"(good ? __uint_as_float(r[c]) : nan)
-                       : "memory");
+          const uint32_t slot = (uint32_t)(rank * width + col) * 512u +
+                                (uint32_t)(quarter * 32 + lane) * 4u * chunk;
+          if (chunk == 4) {
+            cluster_store4(cluster_address(ring, owner) + slot, r[c], r[c + 1], r[c + 2], r[c + 3]);
+          } else {
+            cluster_store2(cluster_address(ring, owner) + slot, r[c], r[c + 1]);
+            cluster_store2(cluster_address(ring, owner + 1) + slot, r[c + 2], r[c + 3]);
+          }
         }
       }
     cluster_sync();
     if (warp >= 4 && warp < 12)
-      for (int c = group; c < width; c += 2) {
+      for (int c = group * chunk; c < width; c += 2 * chunk) {
         const int col = rank * width + c;
-        float sum = 0.f;
-        for (int r = 0; r < split; ++r) {
-          float p;
-          asm volatile("ld.shared.f32 %0, [%1];"
-                       : "=f"(p)
-                       : "r"(ring + ((r * width + c) * 128 + quarter * 32 + lane) * 4)
-                       : "memory");
-          sum += p;
+        float v[16];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          v[e] = 0.f;
+          if (e < chunk)
+            for (int r = 0; r < split; ++r) {
+              float p;
+              asm volatile("ld.shared.f32 %0, [%1];"
+                           : "=f"(p)
+                           : "r"(ring + (r * width + c) * 512 +
+                                 ((quarter * 32 + lane) * chunk + e) * 4)
+                           : "memory");
+              v[e] += p;
+            }
         }
-        if (j0 + col < a.n && i < a.m) {
-          const float v[16] = {sum};
-          store_tokens_any(a, i, j0 + col, 1, v, channel, token_scale + col);
-        }
+        if (j0 + col < a.n && i < a.m)
+          store_tokens_any(a, i, j0 + col, (int)min((long long)chunk, a.n - j0 - col), v, channel,
+                           token_scale + col);
       }
   }
   if (*dead != 0 && threadIdx.x == 0) atomicMax(status, epoch);
