@@ -14,7 +14,6 @@
 
 namespace xsymv {
 
-template <class T>
 struct GemmqArgs {
   int m, n, k;
   float alpha;
@@ -25,36 +24,19 @@ struct GemmqArgs {
   long long ldx;
   const float* sx;
   float beta;
-  T* Y;
+  void* Y;
   long long ldy;
+  char type;   // of Y: 's', 'h' or 'b'
 };
-
-// sx[j] * alpha and sw[i]
-template <class T>
-__device__ __forceinline__ float token_factor(const GemmqArgs<T>& a, long long j) {
+// sx[j] * alpha
+__device__ __forceinline__ float token_factor(const GemmqArgs& a, long long j) {
   return (a.sx != nullptr ? a.sx[j] : 1.f) * a.alpha;
 }
-template <class T>
-__device__ __forceinline__ float channel_factor(const GemmqArgs<T>& a, long long i) {
-  return a.sw != nullptr ? a.sw[i] : 1.f;
-}
-// Y(i, j) := (acc * sw) * (sx * alpha) + beta * Y(i, j), rounded once
-template <class T>
-__device__ __forceinline__ void store_output(const GemmqArgs<T>& a, long long i, long long j,
-                                             float acc, float channel, float token) {
-  float v = acc * channel * token;
-  T* y = a.Y + j * a.ldy + i;
-  if (a.beta != 0.f) v = fmaf(a.beta, to_float(*y), v);
-  *y = from_float<T>(v);
-}
 
-// ... with the type of Y known at run time, for the kernels of a few tokens
-struct GemmqAny : GemmqArgs<void> {
-  char type;   // 's', 'h' or 'b'
-};
-__device__ __forceinline__ void store_any(const GemmqAny& a, long long i, long long j, float acc) {
+// Y(i, j) := (acc * sw) * (sx * alpha) + beta * Y(i, j), rounded once
+__device__ __forceinline__ void store_any(const GemmqArgs& a, long long i, long long j, float acc) {
   const float channel = a.sw != nullptr ? a.sw[i] : 1.f;
-  const float token = (a.sx != nullptr ? a.sx[j] : 1.f) * a.alpha;
+  const float token = token_factor(a, j);
   auto put = [&](auto* y) {
     using T = std::remove_pointer_t<decltype(y)>;
     float v = acc * channel * token;
@@ -101,9 +83,9 @@ __device__ __forceinline__ uint4 load16(const int8_t* row, int first, int k) {
   uint4 z = make_uint4(0, 0, 0, 0);
   if (first >= k) return z;
   const int8_t* at = row + first;
-  // X is read by many warps, W once
+  // X is read by many warps, W once (but off the grid a piece of it by two lanes)
   auto piece = [](const void* p) {
-    return MASK ? __ldg(reinterpret_cast<const uint4*>(p)) : load_once(p);
+    return MASK || !GRID ? __ldg(reinterpret_cast<const uint4*>(p)) : load_once(p);
   };
   if (GRID) return piece(at);
   const unsigned off = (unsigned)(reinterpret_cast<uintptr_t>(at) % 16);
@@ -129,102 +111,15 @@ __device__ __forceinline__ uint4 load16(const int8_t* row, int first, int k) {
   return z;
 }
 
-// Up to 4 tokens: dot products of 8-bit integers (dp4a, 32-bit sums), bound
-// by the bytes of W.  A row of W (a channel) is `threads` threads' work, a power of
-// two from 4 to a whole block, R rows at a time; X comes from L1.
-constexpr int kDotBlock = 256;
-constexpr int kDotMostDepth = 1 << 22;   // a thread's sums stay below 2^31
-template <int NT, int R, bool GRID>
-__global__ void __launch_bounds__(kDotBlock) gemmq_dot(GemmqAny a, int threads) {
-  __shared__ float buf[kDotBlock / 32][R * NT];
-  await_predecessor();
-  const int part = (int)threadIdx.x & (threads - 1);
-  const long long i0 = ((long long)blockIdx.x * (kDotBlock / threads) + threadIdx.x / threads) * R;
-  int acc[R][NT];
-#pragma unroll
-  for (int r = 0; r < R; ++r)
-#pragma unroll
-    for (int t = 0; t < NT; ++t) acc[r][t] = 0;
-  const int8_t *w[R], *x[NT];
-#pragma unroll
-  for (int r = 0; r < R; ++r) w[r] = a.W + min(i0 + r, a.m - 1LL) * a.ldw;
-#pragma unroll
-  for (int t = 0; t < NT; ++t) x[t] = a.X + min(t, a.n - 1) * a.ldx;
-  constexpr int U = 4 / R;   // 64 bytes of W on their way
-  for (int p = part * 16; p < a.k; p += threads * 16 * U) {
-    uint4 q[U][R];
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-      for (int r = 0; r < R; ++r) q[u][r] = load16<GRID, false>(w[r], p + u * threads * 16, a.k);
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        const uint4 v = load16<GRID, true>(x[t], p + u * threads * 16, a.k);
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-          acc[r][t] = __dp4a((int)q[u][r].x, (int)v.x, acc[r][t]);
-          acc[r][t] = __dp4a((int)q[u][r].y, (int)v.y, acc[r][t]);
-          acc[r][t] = __dp4a((int)q[u][r].z, (int)v.z, acc[r][t]);
-          acc[r][t] = __dp4a((int)q[u][r].w, (int)v.w, acc[r][t]);
-        }
-      }
-  }
-  // sums below 2^31 are added as integers, larger ones (k >= 2^17) as floats
-  const bool whole = a.k < 1 << 17;
-  float sum[R][NT];
-#pragma unroll
-  for (int r = 0; r < R; ++r)
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      if (whole) {
-        int v = acc[r][t];
-        for (int o = min(threads, 32) / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-        sum[r][t] = __int_as_float(v);
-      } else {
-        float v = (float)acc[r][t];
-        for (int o = min(threads, 32) / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-        sum[r][t] = v;
-      }
-    }
-  if (threads > 32) {
-    if (threadIdx.x % 32 == 0)
-#pragma unroll
-      for (int r = 0; r < R; ++r)
-#pragma unroll
-        for (int t = 0; t < NT; ++t) buf[threadIdx.x / 32][r * NT + t] = sum[r][t];
-    __syncthreads();
-  }
-  if (part != 0) return;
-#pragma unroll
-  for (int r = 0; r < R; ++r)
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      if (i0 + r >= a.m || t >= a.n) continue;
-      float v;
-      if (whole) {
-        int s = __float_as_int(sum[r][t]);
-        for (int w = 1; w < threads / 32; ++w)
-          s += __float_as_int(buf[threadIdx.x / 32 + w][r * NT + t]);
-        v = (float)s;
-      } else {
-        v = sum[r][t];
-        for (int w = 1; w < threads / 32; ++w) v += buf[threadIdx.x / 32 + w][r * NT + t];
-      }
-      store_any(a, i0 + r, t, v);
-    }
-}
-
-// 5 to 40 tokens: W and X become halves in registers, products on the
-// warp-level tensor path (mma.sync, m16n8k16), whose 1000 multiply-adds a clock and SM
-// keep up with the bytes of W up to about 40 tokens; above, tiles win.  A lane holds
-// 16 consecutive integers of the rows g and g + 8 of a 16-row tile (g =
-// lane / 4) and of token g: the depth is taken in whatever order makes them
-// fragments, the same for W and X.  A warp has 2 row tiles and every 8th
-// part of the depth; the block's 8 warps add their sums in shared memory, in
-// warp order.
-constexpr int kMmaWarps = 8, kMmaRows = 32;
+// Up to 8 tokens: W and X become halves in registers, products on the warp-level
+// tensor path (mma.sync, m16n8k16).  A lane holds 16 consecutive integers of the rows
+// g and g + 8 of a 16-row tile (g = lane / 4) and of token g: the depth is taken in
+// whatever order makes them fragments, the same for W and X.  A block has 2 row tiles;
+// its 8 warps take every 8th 64 of its part of the depth and add their sums in shared
+// memory, in warp order, then the CTAs of a cluster (as many as share the depth
+// where there are few rows) theirs in rank 0's, in rank order.
+constexpr int kFewTokens = 8, kFewMostDepth = 1 << 22;
+constexpr int kMmaWarps = 8, kMmaRows = 32, kFewStep = kMmaWarps * 64;
 __device__ __forceinline__ void mma_16x8x16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                             uint32_t a3, uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -233,303 +128,135 @@ __device__ __forceinline__ void mma_16x8x16(float (&c)[4], uint32_t a0, uint32_t
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-template <int NT8, bool GRID>
-__global__ void __launch_bounds__(kMmaWarps * 32) gemmq_mma(GemmqAny a) {
-  __shared__ float buf[kMmaWarps][kMmaRows][NT8 * 8 + 2];
-  await_predecessor();
+template <bool GRID>
+__global__ void __launch_bounds__(kMmaWarps * 32, 4) gemmq_few(GemmqArgs a, int split) {
+  __shared__ float buf[kMmaWarps][kMmaRows][kFewTokens + 2];
+  __shared__ float parts[8][kFewTokens][kMmaRows];   // of the cluster's CTAs
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
-  const long long i0 = (long long)blockIdx.x * kMmaRows;
-  const int8_t *w[4], *x[NT8];
+  const int rank = split > 1 ? (int)cluster_rank() : 0;
+  const long long i0 = (long long)(blockIdx.x / split) * kMmaRows;
+  // rows g, g + 8, .. of the tile; for those beyond the last row, another one
+  const int8_t* const w0 = a.W + min(i0 + g, a.m - 1LL) * a.ldw;
+  const int left = (int)min((long long)kMmaRows, a.m - i0) - g;
+  const long long down = 8 * a.ldw;
+  auto row = [&](int r) { return 8 * r < left ? w0 + r * down : w0; };
+  const int8_t* const x = a.X + min(g, a.n - 1) * a.ldx;
+  // this CTA's part of the depth: whole steps of the block
+  const int steps = (a.k + kFewStep - 1) / kFewStep;
+  const int end = min(a.k, (int)((long long)steps * (rank + 1) / split) * kFewStep);
+  int p = (int)((long long)steps * rank / split) * kFewStep + warp * 64 + t * 16;
+  // its first integers of W on their way to L2 while the predecessor still runs
 #pragma unroll
-  for (int r = 0; r < 4; ++r) w[r] = a.W + min(i0 + g + 8 * r, a.m - 1LL) * a.ldw;
-#pragma unroll
-  for (int c = 0; c < NT8; ++c) x[c] = a.X + min(g + 8 * c, a.n - 1) * a.ldx;
-  float acc[2][NT8][4];
+  for (int r = 0; r < 4; ++r)
+    if (t == 0 && p < end) asm volatile("prefetch.global.L2 [%0];" ::"l"(row(r) + p));
+  await_predecessor();
+  float acc[2][4];
 #pragma unroll
   for (int h = 0; h < 2; ++h)
 #pragma unroll
-    for (int c = 0; c < NT8; ++c)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) acc[h][c][e] = 0.f;
+    for (int e = 0; e < 4; ++e) acc[h][e] = 0.f;
   uint4 next[4];
-  const int step = kMmaWarps * 64;
-  int p = warp * 64 + t * 16;
 #pragma unroll
-  for (int r = 0; r < 4; ++r) next[r] = load16<GRID, false>(w[r], p, a.k);
-  for (; p - t * 16 < a.k; p += step) {
+  for (int r = 0; r < 4; ++r) next[r] = load16<GRID, false>(row(r), p, end);
+  for (; p - t * 16 < end; p += kFewStep) {
     uint4 q[4];
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       q[r] = next[r];
-      next[r] = load16<GRID, false>(w[r], p + step, a.k);
+      next[r] = load16<GRID, false>(row(r), p + kFewStep, end);
     }
-    uint4 v[NT8];
-#pragma unroll
-    for (int c = 0; c < NT8; ++c) v[c] = load16<GRID, true>(x[c], p, a.k);
+    const uint4 v = load16<GRID, true>(x, p, end);
 #pragma unroll
     for (int s = 0; s < 4; ++s) {   // 4 of the lane's 16 integers
       auto word = [s](const uint4& u) { return s == 0 ? u.x : s == 1 ? u.y : s == 2 ? u.z : u.w; };
-      uint32_t lo[4], hi[4];
+      uint32_t lo[4], hi[4], b0, b1;
 #pragma unroll
       for (int r = 0; r < 4; ++r) halves_of(word(q[r]), lo[r], hi[r]);
-#pragma unroll
-      for (int c = 0; c < NT8; ++c) {
-        uint32_t b0, b1;
-        halves_of(word(v[c]), b0, b1);
-        mma_16x8x16(acc[0][c], lo[0], lo[1], hi[0], hi[1], b0, b1);
-        mma_16x8x16(acc[1][c], lo[2], lo[3], hi[2], hi[3], b0, b1);
-      }
+      halves_of(word(v), b0, b1);
+      mma_16x8x16(acc[0], lo[0], lo[1], hi[0], hi[1], b0, b1);
+      mma_16x8x16(acc[1], lo[2], lo[3], hi[2], hi[3], b0, b1);
     }
   }
 #pragma unroll
-  for (int h = 0; h < 2; ++h)
-#pragma unroll
-    for (int c = 0; c < NT8; ++c) {
-      float* b = &buf[warp][h * 16 + g][c * 8 + 2 * t];
-      b[0] = acc[h][c][0];
-      b[1] = acc[h][c][1];
-      b += 8 * (NT8 * 8 + 2);
-      b[0] = acc[h][c][2];
-      b[1] = acc[h][c][3];
-    }
+  for (int h = 0; h < 2; ++h) {
+    buf[warp][h * 16 + g][2 * t] = acc[h][0];
+    buf[warp][h * 16 + g][2 * t + 1] = acc[h][1];
+    buf[warp][h * 16 + g + 8][2 * t] = acc[h][2];
+    buf[warp][h * 16 + g + 8][2 * t + 1] = acc[h][3];
+  }
   __syncthreads();
-  // lanes along the channels
-  for (int c = warp; c < a.n; c += kMmaWarps) {
-    float v = 0.f;
+  // lanes along the channels, a warp a token
+  float v = 0.f;
 #pragma unroll
-    for (int s = 0; s < kMmaWarps; ++s) v += buf[s][lane][c];
-    if (i0 + lane < a.m) store_any(a, i0 + lane, c, v);
+  for (int s = 0; s < kMmaWarps; ++s) v += buf[s][lane][warp];
+  if (split > 1) {
+    const uint32_t to = cluster_address(smem_addr(&parts[rank][warp][lane]), 0);
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to), "f"(v) : "memory");
+    cluster_sync();
+    if (rank != 0) return;
+    v = 0.f;
+    for (int r = 0; r < split; ++r) v += parts[r][warp][lane];
   }
+  if (warp < a.n && i0 + lane < a.m) store_any(a, i0 + lane, warp, v);
 }
 
-// ------------------------------------------------------ operands as halves --
+// ------------------------------------------------ operands made beforehand --
 
-// Rows of kp halves (a multiple of kDepth, zeros beyond k) from rows of k
-// integers at any alignment: what the tensor copies read.
+// Rows of 8-bit integers at any alignment to rows on 16-byte boundaries, `width`
+// elements long (zeros beyond k): as they are, or as halves.  Both operands of a
+// product in one launch: the first `first_blocks` blocks take `a`'s rows, the others
+// `b`'s, `along` threads a row.
 constexpr int kDepth = 64;   // 128 bytes of halves
-template <bool GRID>
-__global__ void __launch_bounds__(256) halves_kernel(int rows, int k, int kp, const int8_t* q,
-                                                     long long ldq, __half* out) {
-  await_predecessor();
-  const long long j = blockIdx.x * (long long)blockDim.y + threadIdx.y;
-  if (j >= rows) return;
-  q += j * ldq;
-  out += j * kp;
-  for (int first = (int)(blockIdx.y * blockDim.x + threadIdx.x) * kPack; first < kp;
-       first += (int)(gridDim.y * blockDim.x) * kPack) {
-    const Raw<int8_t> r = load8<GRID>(q, first, k);
-    uint4 h;
-    halves_of(r.w[0], h.x, h.y);
-    halves_of(r.w[1], h.z, h.w);
-    *reinterpret_cast<uint4*>(out + first) = h;
-  }
-}
-
-// ... and rows of 8-bit integers on 16-byte boundaries, ldo a multiple of 16
-__global__ void __launch_bounds__(256) align_kernel(int rows, int k, const int8_t* q, long long ldq,
-                                                    int8_t* out, long long ldo) {
-  await_predecessor();
-  const long long j = blockIdx.x * (long long)blockDim.y + threadIdx.y;
-  if (j >= rows) return;
-  q += j * ldq;
-  out += j * ldo;
-  for (int first = (int)(blockIdx.y * blockDim.x + threadIdx.x) * kPack; first < ldo;
-       first += (int)(gridDim.y * blockDim.x) * kPack) {
-    const Raw<int8_t> r = load8<false>(q, first, k);
-    *reinterpret_cast<uint2*>(out + first) = make_uint2(r.w[0], r.w[1]);
-  }
-}
-
-// ------------------------------------------------------- the tiled product --
-
-// A tile is 128 channels by BN tokens, or 256 by BN shared by a pair of CTAs
-// (each holds its 128 channels' and half of the tokens' operands, and the
-// accumulators of its channels).  Channels are the rows of the accumulator:
-// a lane holds one channel and stores of 32 lanes side by side need no
-// alignment.  Warp 0 copies, warp 1 multiplies (the pair's first CTA alone),
-// warps 2 to 5 store a tile from one set of accumulators while the next is
-// formed in the other.
-template <int CTAS, int BN>
-struct Tile {
-  static constexpr int kChannels = 128 * CTAS, kTokens = BN;
-  static constexpr int kBytesW = 128 * kDepth * 2, kBytesX = BN / CTAS * kDepth * 2;
-  static constexpr int kStageBytes = kBytesW + kBytesX;
-  static constexpr int kStages = 196608 / kStageBytes;
-  static constexpr int kColumns = 2 * BN;   // of tensor memory
-  static constexpr int kThreads = 192;
-  static constexpr int kSmem = kStages * kStageBytes + 1024;
+struct Prepare {
+  const int8_t* q;
+  long long ldq;
+  int rows, k;
+  long long width;   // a multiple of 16
+  void* out;         // width apart
+  bool halves, grid;
+  int along;
 };
-
-struct TileOrder {
-  int tiles_m, tiles_n, tiles;
-  // Tiles that run at the same time are near one another in both directions:
-  // bands of 8 tiles of tokens, channels advancing within a band
-  __device__ __forceinline__ void at(int t, int& tm, int& tn) const {
-    const int band = 8 * tiles_m, b = t / band, in = t - b * band;
-    const int width = min(8, tiles_n - 8 * b);
-    tm = in / width;
-    tn = 8 * b + in - tm * width;
-  }
-};
-
-template <class T, int CTAS, int BN>
-__global__ void __launch_bounds__(192, 1)
-    gemmq_tiles(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
-                GemmqArgs<T> a, TileOrder order, int steps, int* status, int epoch,
-                unsigned long long limit_ns, uint32_t extra_tx) {
-  using S = Tile<CTAS, BN>;
-  extern __shared__ uint8_t raw_smem[];
-  __shared__ alignas(8) uint64_t bar_words[2 * S::kStages + 4];
-  __shared__ uint32_t tmem_word;
-  __shared__ int dead_word;
-  __shared__ float token_scale[2][BN];
-  volatile int* const dead = &dead_word;
-  const uint32_t tiles_smem = (smem_addr(raw_smem) + 1023u) & ~1023u;
-  const uint32_t full = smem_addr(bar_words), empty = full + 8 * S::kStages;
-  const uint32_t acc_full = empty + 8 * S::kStages, acc_empty = acc_full + 16;
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const uint32_t rank = CTAS == 2 ? cluster_rank() : 0;
-  const int first_tile = blockIdx.x / CTAS, stride = gridDim.x / CTAS;
-
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < S::kStages; ++s) {
-      mbar_init(full + 8 * s, 1);
-      mbar_init(empty + 8 * s, 1);
-    }
-    for (int b = 0; b < 2; ++b) {
-      mbar_init(acc_full + 8 * b, 1);
-      mbar_init(acc_empty + 8 * b, 4 * CTAS);
-    }
-    dead_word = 0;
-    mbar_init_fence();
-  }
-  if (warp == 1) tmem_alloc<CTAS>(smem_addr(&tmem_word), S::kColumns);
-  tensor_fence_before();
-  __syncthreads();
-  if (CTAS == 2) cluster_sync();
-  tensor_fence_after();
-  const uint32_t tmem = tmem_word;
+__global__ void __launch_bounds__(256) prepare_kernel(Prepare a, Prepare b, int first_blocks) {
   await_predecessor();
-
-  if (warp == 0 && lane == 0) {
-    // ---- copies: this CTA's channels and its share of the tokens
-    const uint32_t lead_full = CTAS == 2 ? cluster_address(full, 0) : full;
-    int stage = 0, issued = 0;
-    uint32_t phase = 0;
-    bool ok = true;
-    for (int t = first_tile; ok && t < order.tiles; t += stride) {
-      int tm, tn;
-      order.at(t, tm, tn);
-      const int row_w = tm * S::kChannels + (int)rank * 128;
-      const int row_x = tn * BN + (int)rank * (BN / CTAS);
-      for (int s = 0; s < steps; ++s) {
-        if (!wait_or_dead(empty + 8 * stage, phase ^ 1, dead, limit_ns)) {
-          ok = false;
-          break;
-        }
-        if (rank == 0)
-          mbar_arrive_expect_tx(full + 8 * stage, CTAS * S::kStageBytes + extra_tx);
-        const uint32_t at = tiles_smem + stage * S::kStageBytes;
-        tensor_g2s<CTAS>(at, &map_w, s * kDepth, row_w, lead_full + 8 * stage);
-        tensor_g2s<CTAS>(at + S::kBytesW, &map_x, s * kDepth, row_x, lead_full + 8 * stage);
-        issued = min(issued + 1, S::kStages);
-        if (++stage == S::kStages) stage = 0, phase ^= 1;
-      }
-    }
-    // Every copy has landed, and every product that reads it is done, before
-    // shared memory is given back: the last stages' empty barriers
-    const unsigned long long t0 = global_ns();
-    for (int s = 0; s < issued; ++s) {
-      stage = stage == 0 ? S::kStages - 1 : stage - 1;
-      if (stage == S::kStages - 1) phase ^= 1;
-      while (!mbar_try_wait(empty + 8 * stage, phase))
-        if (global_ns() - t0 > limit_ns) {
-          *dead = 1;
-          ok = false;
-          break;
-        }
-    }
-    if (!ok || *dead != 0) atomicMax(status, epoch);
-  } else if (warp == 1 && rank == 0) {
-    // ---- products
-    constexpr uint32_t idesc = half_mma(S::kChannels, BN);
-    const uint32_t one = elect_one();
-    int stage = 0, set = 0;
-    uint32_t phase = 0, set_phase = 0;
-    bool ok = true;
-    for (int t = first_tile; ok && t < order.tiles; t += stride) {
-      ok = __all_sync(0xffffffffu, wait_or_dead(acc_empty + 8 * set, set_phase ^ 1, dead, limit_ns));
-      if (!ok) break;
-      tensor_fence_after();
-      for (int s = 0; s < steps; ++s) {
-        ok = __all_sync(0xffffffffu, wait_or_dead(full + 8 * stage, phase, dead, limit_ns));
-        if (!ok) break;
-        tensor_fence_after();
-        const uint32_t at = tiles_smem + stage * S::kStageBytes;
-        const uint64_t dw = tile_descriptor(at), dx = tile_descriptor(at + S::kBytesW);
+  const bool second = (int)blockIdx.x >= first_blocks;
+  const Prepare c = second ? b : a;
+  const int per_block = 256 / c.along, x = (int)threadIdx.x & (c.along - 1);
+  const long long j = ((long long)blockIdx.x - (second ? first_blocks : 0)) * per_block +
+                      (int)threadIdx.x / c.along;
+  if (j >= c.rows) return;
+  const int8_t* q = c.q + j * c.ldq;
+  constexpr int U = 4;
+  for (long long p = x * 16LL; p < c.width; p += (long long)c.along * 16 * U) {
+    uint4 v[U];
 #pragma unroll
-        for (int q = 0; q < kDepth / 16; ++q)   // 16 halves: 32 bytes, 2 units of the descriptor
-          mma_half<CTAS>(tmem + set * BN, dw + 2 * q, dx + 2 * q, idesc, s > 0 || q > 0, one);
-        mma_commit<CTAS>(empty + 8 * stage, one);
-        if (++stage == S::kStages) stage = 0, phase ^= 1;
-      }
-      if (ok) mma_commit<CTAS>(acc_full + 8 * set, one);
-      set ^= 1;
-      if (set == 0) set_phase ^= 1;
+    for (int u = 0; u < U; ++u) {
+      const long long at = p + (long long)u * c.along * 16;
+      if (at < c.width)
+        v[u] = c.grid ? load16<true, true>(q, (int)at, c.k) : load16<false, true>(q, (int)at, c.k);
     }
-    if (*dead != 0 && lane == 0) atomicMax(status, epoch);
-  } else if (warp >= 2) {
-    // ---- results: a warp may read the 32 lanes of tensor memory of its number mod 4
-    const int quarter = warp % 4;
-    const uint32_t lead_empty = CTAS == 2 ? cluster_address(acc_empty, 0) : acc_empty;
-    int set = 0;
-    uint32_t set_phase = 0;
-    bool ok = true;
-    for (int t = first_tile; t < order.tiles; t += stride) {
-      int tm, tn;
-      order.at(t, tm, tn);
-      const long long i = (long long)tm * S::kChannels + (int)rank * 128 + quarter * 32 + lane;
-      const long long j0 = (long long)tn * BN;
-      for (int c = (int)threadIdx.x - 64; c < BN; c += 128)
-        token_scale[set][c] = j0 + c < a.n ? token_factor(a, j0 + c) : 0.f;
-      const float channel = i < a.m ? channel_factor(a, i) : 0.f;
-      if (ok && !wait_or_dead(acc_full + 8 * set, set_phase, dead, limit_ns)) ok = false;
-      ok = __all_sync(0xffffffffu, ok);
-      asm volatile("bar.sync 1, 128;" ::: "memory");   // token_scale is complete
-      tensor_fence_after();
-      for (int c0 = 0; c0 < BN && j0 + c0 < a.n; c0 += 32) {
-        uint32_t r[32];
-        tmem_load32(r, tmem + ((uint32_t)(quarter * 32) << 16) + set * BN + c0);
-        if (i < a.m) {
 #pragma unroll
-          for (int c = 0; c < 32; ++c)
-            if (j0 + c0 + c < a.n)
-              store_output(a, i, j0 + c0 + c,
-                           ok ? __uint_as_float(r[c]) : __uint_as_float(0x7fc00000u), channel,
-                           token_scale[set][c0 + c]);
-        }
-        __syncwarp();
+    for (int u = 0; u < U; ++u) {
+      const long long at = p + (long long)u * c.along * 16;
+      if (at >= c.width) continue;
+      if (c.halves) {
+        uint4* to = reinterpret_cast<uint4*>(static_cast<__half*>(c.out) + j * c.width + at);
+        uint4 h;
+        halves_of(v[u].x, h.x, h.y);
+        halves_of(v[u].y, h.z, h.w);
+        to[0] = h;
+        halves_of(v[u].z, h.x, h.y);
+        halves_of(v[u].w, h.z, h.w);
+        to[1] = h;
+      } else {
+        *reinterpret_cast<uint4*>(static_cast<int8_t*>(c.out) + j * c.width + at) = v[u];
       }
-      tensor_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(lead_empty + 8 * set);
-      set ^= 1;
-      if (set == 0) set_phase ^= 1;
     }
-    if (!ok && lane == 0) atomicMax(status, epoch);
   }
-  __syncwarp();
-  tensor_fence_before();
-  __syncthreads();
-  if (CTAS == 2) cluster_sync();
-  tensor_fence_after();
-  if (warp == 1) tmem_free<CTAS>(tmem, S::kColumns);
 }
 
-// ------------------------------------------- tiles with W as it is stored --
+// ------------------------------------------------ tiles on the tensor cores --
 
-// From 9 tokens to a few thousand, where converting W beforehand would cost more than
-// the product: W reaches shared memory as 8-bit integers, eight warps make
+// From 9 tokens on: W reaches shared memory as 8-bit integers, eight warps make
 // halves of it on the way to tensor memory, and the tensor cores take their
 // first operand from there.  (In shared memory the halves would cost four
 // times their 8-bit bytes of its bandwidth, more than an SM has at the rate W
@@ -538,25 +265,24 @@ __global__ void __launch_bounds__(192, 1)
 // share a tile's depth when there are few tiles and add their accumulators
 // through each other's shared memory, in rank order.
 //
-// Up to 64 tokens X too arrives as 8-bit integers and four more warps make its
-// halves in shared memory (RAW): the call is one kernel.  Wider tiles read halves
-// that halves_kernel made: made here they would cost shared memory twice the traffic.
+// RAW: X too arrives as 8-bit integers and four more warps make its halves in shared
+// memory, so the call is one kernel.  Else X's halves come from prepare_kernel.
 //
 // Warp 0 copies W, warp 1 copies X, warp 2 multiplies, warp 3 holds the tensor memory,
 // warps 4 to 11 convert W and store the results, warps 12 to 15 (RAW) convert X.
 constexpr int kStepDepth = 128;   // of a step: 128 bytes of W, 256 of X's halves
-template <int CTAS, int BN>
+template <int CTAS, int BN, bool RAW>
 struct Stream {
-  static constexpr bool kRaw = BN <= 64;   // and two CTAs an SM
+  static constexpr bool kTwice = BN <= 64;   // two CTAs an SM
   static constexpr int kChannels = 128 * CTAS;
   static constexpr int kBytesW = 128 * kStepDepth, kHalfX = BN / CTAS * 128;
-  static constexpr int kBytesX = 2 * kHalfX, kBytesRaw = kRaw ? BN * kStepDepth : 0;
+  static constexpr int kBytesX = 2 * kHalfX, kBytesRaw = RAW ? BN * kStepDepth : 0;
   // steps of W, of X's halves and of W's halves in tensor memory, of raw X
-  static constexpr int kStagesA = kRaw ? 2 : 4, kStagesX = kStagesA, kStagesRaw = kRaw ? 2 : 0;
-  static constexpr int kStagesW = kRaw ? (BN == 64 ? 3 : 5) : 4;
+  static constexpr int kStagesA = kTwice ? 2 : 4, kStagesX = kStagesA, kStagesRaw = RAW ? 2 : 0;
+  static constexpr int kStagesW = !kTwice ? 4 : BN == 64 && RAW ? 3 : 4;
   static constexpr int kColumnsA = kStepDepth / 2;
-  static constexpr int kColumns = kRaw ? 256 : 512;
-  static constexpr int kThreads = kRaw ? 512 : 384;
+  static constexpr int kColumns = kTwice ? 256 : 512;
+  static constexpr int kThreads = RAW ? 512 : 384;
   static constexpr int kAtX = kStagesW * kBytesW, kAtRaw = kAtX + kStagesX * kBytesX;
   static constexpr int kRing = kAtRaw + kStagesRaw * kBytesRaw;
   static constexpr int kSmem = kRing + 1024;
@@ -568,15 +294,20 @@ struct Stream {
 template <class T>
 __device__ __forceinline__ void store_tokens(T* y, long long ldy, int count, const float (&v)[16],
                                              float channel, const float* token, float beta) {
+  if (count == 16 && beta == 0.f) {
 #pragma unroll
-  for (int c = 0; c < 16; ++c)
-    if (c < count) {
-      float r = v[c] * channel * token[c];
-      if (beta != 0.f) r = fmaf(beta, to_float(y[c * ldy]), r);
-      y[c * ldy] = from_float<T>(r);
-    }
+    for (int c = 0; c < 16; ++c, y += ldy) *y = from_float<T>(v[c] * channel * token[c]);
+  } else {
+#pragma unroll
+    for (int c = 0; c < 16; ++c, y += ldy)
+      if (c < count) {
+        float r = v[c] * channel * token[c];
+        if (beta != 0.f) r = fmaf(beta, to_float(*y), r);
+        *y = from_float<T>(r);
+      }
+  }
 }
-__device__ __forceinline__ void store_tokens_any(const GemmqAny& a, long long i, long long j,
+__device__ __forceinline__ void store_tokens_any(const GemmqArgs& a, long long i, long long j,
                                                  int count, const float (&v)[16], float channel,
                                                  const float* token) {
   const long long at = j * a.ldy + i;
@@ -588,14 +319,14 @@ __device__ __forceinline__ void store_tokens_any(const GemmqAny& a, long long i,
     store_tokens(static_cast<__nv_bfloat16*>(a.Y) + at, a.ldy, count, v, channel, token, a.beta);
 }
 
-template <int CTAS, int BN>
-__global__ void __launch_bounds__(Stream<CTAS, BN>::kThreads, Stream<CTAS, BN>::kRaw ? 2 : 1)
+template <int CTAS, int BN, bool RAW>
+__global__ void __launch_bounds__(Stream<CTAS, BN, RAW>::kThreads,
+                                  Stream<CTAS, BN, RAW>::kTwice ? 2 : 1)
     gemmq_stream(const __grid_constant__ CUtensorMap map_w,
-                 const __grid_constant__ CUtensorMap map_x, GemmqAny a, int tiles_n, int steps,
+                 const __grid_constant__ CUtensorMap map_x, GemmqArgs a, int tiles_n, int steps,
                  int split, int* status, int epoch, unsigned long long limit_ns,
                  uint32_t extra_tx) {
-  using S = Stream<CTAS, BN>;
-  constexpr bool RAW = S::kRaw;
+  using S = Stream<CTAS, BN, RAW>;
   // the ring that X's copies fill: raw X, or its halves
   constexpr int COPIES = RAW ? S::kStagesRaw : S::kStagesX;
   extern __shared__ uint8_t raw_smem[];
@@ -621,7 +352,7 @@ __global__ void __launch_bounds__(Stream<CTAS, BN>::kThreads, Stream<CTAS, BN>::
   const int s0 = (int)((long long)steps * part / split);
   const int mine = (int)((long long)steps * (part + 1) / split) - s0;
 
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (CTAS == 1) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (threadIdx.x == 0) {
     // the first steps of W on their way to L2 while the predecessor still runs
     for (int u = 0; u < min(mine, 8); ++u)
