@@ -207,12 +207,16 @@ def _uplo(u) -> bytes:
 
 
 _cuda_ok = None          # torch's CUDA availability, asked once
+_raw_stream = None       # torch's lookups of a device's current stream and of the
+_current_device = None   # current device, once it is known to have a GPU
 
 
 def _torch_stream():
     """torch's current CUDA stream on the current device, as an address
     (None when torch is not loaded or has no GPU)"""
-    global _cuda_ok
+    global _cuda_ok, _raw_stream, _current_device
+    if _raw_stream is not None:
+        return _raw_stream(_current_device())
     torch = sys.modules.get("torch")
     if torch is None:
         return None
@@ -222,7 +226,8 @@ def _torch_stream():
         return None
     raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
     if raw is not None:
-        return raw(torch._C._cuda_getDevice())
+        _raw_stream, _current_device = raw, torch._C._cuda_getDevice
+        return raw(_current_device())
     return torch.cuda.current_stream().cuda_stream
 
 
@@ -513,25 +518,33 @@ def xgemv_selected_variant(kind: str) -> int:
 
 # ------------------------------------------- a linear layer in 8 bits -----
 
-def _q8_call(name, kind, stream):
+_q8_entries = {}        # (name, kind): entry point, once looked up
+
+
+def _q8_entry(name, kind, stream):
     """The entry point of `name` for kind ('s' float, 'h' half, 'b' bfloat16),
     with the stream set."""
-    if kind not in ("s", "h", "b"):
-        raise ValueError("kind must be 's', 'h' or 'b'")
-    lib = _lib if _lib is not None else load()
-    _use_stream(lib, stream)
-    return getattr(lib, name + kind)
+    fn = _q8_entries.get((name, kind))
+    if fn is None:
+        if kind not in ("s", "h", "b"):
+            raise ValueError("kind must be 's', 'h' or 'b'")
+        fn = _q8_entries[name, kind] = getattr(load(), name + kind)
+    if stream is None and _raw_stream is not None:      # _use_stream, without the call
+        if _raw_stream(_current_device()) == _stream_set[0]:
+            return fn
+    _use_stream(_lib, stream)
+    return fn
 
 
 def quant(kind, m, n, X, ldx, Q, ldq, scale, stream=None) -> int:
     """The n columns of m elements of X to 8 bits (Q) with a scale each:
     scale[j] = max|X(:,j)| / 127, Q = X / scale rounded to nearest even."""
-    return _q8_call("xquant_", kind, stream)(m, n, _ptr(X), ldx, _ptr(Q), ldq, _ptr(scale))
+    return _q8_entry("xquant_", kind, stream)(m, n, _ptr(X), ldx, _ptr(Q), ldq, _ptr(scale))
 
 
 def dequant(kind, m, n, Q, ldq, scale, X, ldx, stream=None) -> int:
     """X(i,j) = Q(i,j) * scale[j], rounded to kind."""
-    return _q8_call("xdequant_", kind, stream)(m, n, _ptr(Q), ldq, _ptr(scale), _ptr(X), ldx)
+    return _q8_entry("xdequant_", kind, stream)(m, n, _ptr(Q), ldq, _ptr(scale), _ptr(X), ldx)
 
 
 def rmsquant(kind, m, n, X, ldx, R, ldr, G, eps, H, ldh, Q, ldq, scale, rstd,
@@ -539,7 +552,7 @@ def rmsquant(kind, m, n, X, ldx, R, ldr, G, eps, H, ldh, Q, ldq, scale, rstd,
     """H = X + R (R may be None), its root-mean-square norm over each column
     times G (None: ones), quantised to Q and scale.  H and rstd may be None;
     H may be X or R."""
-    return _q8_call("xrmsquant_", kind, stream)(
+    return _q8_entry("xrmsquant_", kind, stream)(
         m, n, _ptr(X), ldx, _ptr(R), ldr, _ptr(G), eps, _ptr(H), ldh, _ptr(Q), ldq, _ptr(scale),
         _ptr(rstd))
 
@@ -549,7 +562,7 @@ def rmsgrad(kind, m, n, dY, lddy, H, ldh, G, rstd, dR, lddr, dX, lddx, dG, strea
     respect to X and R alike) from dY (the norm's output) and dR (H itself,
     may be None), and dG (float, may be None), from the H and rstd that
     rmsquant stored."""
-    return _q8_call("xrmsgrad_", kind, stream)(
+    return _q8_entry("xrmsgrad_", kind, stream)(
         m, n, _ptr(dY), lddy, _ptr(H), ldh, _ptr(G), _ptr(rstd), _ptr(dR), lddr, _ptr(dX), lddx,
         _ptr(dG))
 
@@ -557,7 +570,7 @@ def rmsgrad(kind, m, n, dY, lddy, H, ldh, G, rstd, dR, lddr, dX, lddx, dG, strea
 def gemmq(kind, m, n, k, alpha, W, ldw, sw, X, ldx, sx, beta, Y, ldy, stream=None) -> int:
     """Y := alpha * diag(sw) W^T X diag(sx) + beta * Y with W (k by m) and X
     (k by n) of 8-bit integers, sw and sx float (None: ones), Y of kind."""
-    return _q8_call("xgemmq_", kind, stream)(
+    return _q8_entry("xgemmq_", kind, stream)(
         m, n, k, alpha, _ptr(W), ldw, _ptr(sw), _ptr(X), ldx, _ptr(sx), beta, _ptr(Y), ldy)
 
 

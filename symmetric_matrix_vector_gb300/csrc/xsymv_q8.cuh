@@ -270,16 +270,18 @@ inline cudaError_t launch_after(void (*kernel)(P...), dim3 grid, dim3 block, siz
   return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
 }
 
-// host: the end of a call that launched `kernels` kernels, none of which
-// has a bounded wait.  Noting the call also tells a following SYMV call
-// that its predecessor is not a SYMV finaliser it could overlap with.
-inline int launched(cudaError_t e, int kernels, cudaStream_t st) {
+// host: the end of a call that launched `kernels` kernels; status and epoch:
+// where its bounded waits report, if it has any.  Noting the call also tells a
+// following SYMV call that its predecessor is not a SYMV finaliser it could
+// overlap with.
+inline int launched(cudaError_t e, int kernels, cudaStream_t st, const int* status = nullptr,
+                    int epoch = 0) {
   if (e != cudaSuccess) {
     record_cuda_error(e);
     return XSYMV_ERR_CUDA;
   }
   note_launches(kernels);
-  note_call_status(st, nullptr, 0);
+  note_call_status(st, status, epoch);
   return XSYMV_OK;
 }
 

@@ -1,6 +1,7 @@
 // Entry points xgemmq_s / _h / _b: Y := alpha*diag(sw)*W^T*X*diag(sx) + beta*Y
 // with W and X of 8-bit integers.
 #include <algorithm>
+#include <atomic>
 
 #include "xsymv_q8_gemm.cuh"
 
@@ -90,11 +91,6 @@ struct Pieces {
 template <class... P, class... A>
 cudaError_t launch_cluster(void (*kernel)(P...), unsigned grid, int cluster, int threads, int smem,
                            bool early, cudaStream_t st, A... args) {
-  if (smem > 48 * 1024) {
-    const cudaError_t e =
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(threads);
@@ -117,6 +113,20 @@ cudaError_t launch_cluster(void (*kernel)(P...), unsigned grid, int cluster, int
 
 int* status_word(cudaStream_t st, int* status, int* epoch) {
   return static_cast<int*>(workspace(256, st, status, 0, epoch));
+}
+
+// lets the kernel have its shared memory, once for each device
+template <int CTAS, int BN, bool RAW>
+cudaError_t allow_smem() {
+  static std::atomic<unsigned long long> done{0};
+  const int d = current_device_index();
+  const unsigned long long bit = d >= 0 ? 1ull << d : 0;
+  if (bit != 0 && (done.load() & bit) != 0) return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(
+      gemmq_stream<CTAS, BN, RAW>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+      Stream<CTAS, BN, RAW>::kSmem);
+  if (e == cudaSuccess) done.fetch_or(bit);
+  return e;
 }
 
 template <int CTAS, int BN, bool RAW>
@@ -166,6 +176,7 @@ int gemmq_streamed(const GemmqArgs& a, int split, cudaStream_t st) {
     e = launch_prepare(pw, px, st);
     ++kernels;
   }
+  if (e == cudaSuccess) e = allow_smem<CTAS, BN, RAW>();
   if (e == cudaSuccess) {
     const long long tiles_m = (a.m + S::kChannels - 1LL) / S::kChannels;
     const long long tiles_n = (a.n + BN - 1LL) / BN;
@@ -174,9 +185,7 @@ int gemmq_streamed(const GemmqArgs& a, int split, cudaStream_t st) {
                        S::kThreads, S::kSmem, CTAS == 1, st, map_w, map_x, a, (int)tiles_n, steps, split, word,
                        epoch, wait_limit_ns(), test_extra_tx());
   }
-  const int r = launched(e, kernels, st);
-  if (r == XSYMV_OK) note_call_status(st, word, epoch);
-  return r;
+  return launched(e, kernels, st, word, epoch);
 }
 
 // CTAs that share a tile's depth: twice as many while they all fit on the SMs
