@@ -230,7 +230,6 @@ int gemmq_entry(char type, int m, int n, int k, float alpha, const int8_t* W, in
   const long long rows = (m + 127LL) / 128;   // tiles of 128 channels
   if (n <= 64) {
     const int split = depth_split(rows, steps, 2LL * sms);
-    if (n <= 16) return gemmq_streamed<1, 16, true>(a, split, st);
     if (n <= 32) return gemmq_streamed<1, 32, true>(a, split, st);
     // X's halves made in the tile's CTAs or once beforehand (64 tokens; 4096 x 4096: 11.5
     // against 13.1 us, 32768 x 8192: 63 against 53)

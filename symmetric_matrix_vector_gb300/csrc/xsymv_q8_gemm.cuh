@@ -33,17 +33,15 @@ __device__ __forceinline__ float token_factor(const GemmqArgs& a, long long j) {
   return (a.sx != nullptr ? a.sx[j] : 1.f) * a.alpha;
 }
 
-// Y(i, j) := (acc * sw) * (sx * alpha) + beta * Y(i, j), rounded once
+// Y(i, j) := (acc * sw) * (sx * alpha) + beta * Y(i, j)
 __device__ __forceinline__ void store_any(const GemmqArgs& a, long long i, long long j, float acc) {
   const float channel = a.sw != nullptr ? a.sw[i] : 1.f;
-  const float token = token_factor(a, j);
+  const float v = acc * channel * token_factor(a, j);
+  const long long at = j * a.ldy + i;
   auto put = [&](auto* y) {
     using T = std::remove_pointer_t<decltype(y)>;
-    float v = acc * channel * token;
-    if (a.beta != 0.f) v = fmaf(a.beta, to_float(*y), v);
-    *y = from_float<T>(v);
+    *y = from_float<T>(a.beta != 0.f ? fmaf(a.beta, to_float(*y), v) : v);
   };
-  const long long at = j * a.ldy + i;
   if (a.type == 's')
     put(static_cast<float*>(a.Y) + at);
   else if (a.type == 'h')
@@ -279,7 +277,7 @@ struct Stream {
   static constexpr int kBytesX = 2 * kHalfX, kBytesRaw = RAW ? BN * kStepDepth : 0;
   // steps of W, of X's halves and of W's halves in tensor memory, of raw X
   static constexpr int kStagesA = kTwice ? 2 : 4, kStagesX = kStagesA, kStagesRaw = RAW ? 2 : 0;
-  static constexpr int kStagesW = !kTwice ? 4 : BN == 64 && RAW ? 3 : 4;
+  static constexpr int kStagesW = BN == 64 && RAW ? 3 : 4;
   static constexpr int kColumnsA = kStepDepth / 2;
   static constexpr int kColumns = kTwice ? 256 : 512;
   static constexpr int kThreads = RAW ? 512 : 384;
@@ -290,33 +288,88 @@ struct Stream {
   static_assert(BN * 128 * 4 <= kRing, "the exchange of sums");
 };
 
-// v[c] * channel * token[c] + beta * y[c] to `count` of 16 tokens of a channel
+// A whole depth's sums, straight from tensor memory: this warp's 32 channels, 16 tokens of
+// `width` at a time from `first` on, every `step`-th 16.  (Through shared memory, as
+// below, the stores are wider but 8192 x 8192 x 2048 takes 191 us instead of 180.)
 template <class T>
-__device__ __forceinline__ void store_tokens(T* y, long long ldy, int count, const float (&v)[16],
-                                             float channel, const float* token, float beta) {
-  if (count == 16 && beta == 0.f) {
+__device__ __forceinline__ void store_columns(const GemmqArgs& a, uint32_t tmem, long long i,
+                                              long long j, int first, int step, int width,
+                                              float channel, const float* token) {
+  T* y = static_cast<T*>(a.Y) + (j + first) * a.ldy + i;
+#pragma unroll 1
+  for (int c0 = first; c0 < width && j + c0 < a.n; c0 += step, y += step * a.ldy) {
+    uint32_t r[16];
+    tmem_load16(r, tmem + c0);
+    T* to = y;
+    if (i < a.m && j + c0 + 16 <= a.n && a.beta == 0.f) {
 #pragma unroll
-    for (int c = 0; c < 16; ++c, y += ldy) *y = from_float<T>(v[c] * channel * token[c]);
-  } else {
+      for (int c = 0; c < 16; ++c, to += a.ldy)
+        *to = from_float<T>(__uint_as_float(r[c]) * channel * token[c0 + c]);
+    } else if (i < a.m) {
 #pragma unroll
-    for (int c = 0; c < 16; ++c, y += ldy)
-      if (c < count) {
-        float r = v[c] * channel * token[c];
-        if (beta != 0.f) r = fmaf(beta, to_float(*y), r);
-        *y = from_float<T>(r);
-      }
+      for (int c = 0; c < 16; ++c, to += a.ldy)
+        if (j + c0 + c < a.n) {
+          const float v = __uint_as_float(r[c]) * channel * token[c0 + c];
+          *to = from_float<T>(a.beta != 0.f ? fmaf(a.beta, to_float(*to), v) : v);
+        }
+    }
+    __syncwarp();
   }
 }
-__device__ __forceinline__ void store_tokens_any(const GemmqArgs& a, long long i, long long j,
-                                                 int count, const float (&v)[16], float channel,
-                                                 const float* token) {
-  const long long at = j * a.ldy + i;
-  if (a.type == 's')
-    store_tokens(static_cast<float*>(a.Y) + at, a.ldy, count, v, channel, token, a.beta);
-  else if (a.type == 'h')
-    store_tokens(static_cast<__half*>(a.Y) + at, a.ldy, count, v, channel, token, a.beta);
-  else
-    store_tokens(static_cast<__nv_bfloat16*>(a.Y) + at, a.ldy, count, v, channel, token, a.beta);
+
+// A CTA's share of a tile, in shared memory: `split` sets of sums to be added, each
+// `width` tokens from j on of 128 channels from i on, as [token / 4][channel][token % 4]
+struct TileResult {
+  uint32_t at;
+  int split, width, i;
+  long long j;
+  const float *channel, *token;   // their factors
+  bool failed;
+};
+// ... added, scaled and stored by all warps, 4 tokens of 32 * P channels at a time (P = 2:
+// two 16-bit results a lane, in one 4-byte store)
+template <class T, int P>
+__device__ __forceinline__ void store_result(const GemmqArgs& a, const TileResult& t, int threads) {
+  const int warps = threads / 32, lane = threadIdx.x % 32, across = 4 / P;
+#pragma unroll 1
+  for (int u = threadIdx.x / 32; u < t.width / 4 * across; u += warps) {
+    const int c = u / across * 4, at = (u % across * 32 + lane) * P;
+    float v[P][4];
+#pragma unroll
+    for (int q = 0; q < P; ++q) {
+      const uint32_t from = t.at + (uint32_t)(c * 128 + (at + q) * 4) * 4u;
+      const uint4 p = lds128(from);
+      v[q][0] = __uint_as_float(p.x), v[q][1] = __uint_as_float(p.y);
+      v[q][2] = __uint_as_float(p.z), v[q][3] = __uint_as_float(p.w);
+#pragma unroll 1
+      for (int r = 1; r < t.split; ++r) {
+        const uint4 o = lds128(from + (uint32_t)(r * t.width) * 512u);
+        v[q][0] += __uint_as_float(o.x), v[q][1] += __uint_as_float(o.y);
+        v[q][2] += __uint_as_float(o.z), v[q][3] += __uint_as_float(o.w);
+      }
+      const float channel = t.failed ? __uint_as_float(0x7fc00000u) : t.channel[at + q];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[q][e] *= channel;
+    }
+    const long long i = (long long)t.i + at;
+    T* y = static_cast<T*>(a.Y) + (t.j + c) * a.ldy + i;
+    const bool both = i + P <= a.m;
+#pragma unroll
+    for (int e = 0; e < 4; ++e, y += a.ldy) {
+      if (t.j + c + e >= a.n || i >= a.m) break;
+      T r[P];
+#pragma unroll
+      for (int q = 0; q < P; ++q) {
+        float x = v[q][e] * t.token[c + e];
+        if (a.beta != 0.f && i + q < a.m) x = fmaf(a.beta, to_float(y[q]), x);
+        r[q] = from_float<T>(x);
+      }
+      if (P == 2 && both)
+        *reinterpret_cast<uint32_t*>(y) = *reinterpret_cast<const uint32_t*>(r);
+      else
+        y[0] = r[0];
+    }
+  }
 }
 
 template <int CTAS, int BN, bool RAW>
@@ -333,7 +386,7 @@ __global__ void __launch_bounds__(Stream<CTAS, BN, RAW>::kThreads,
   __shared__ alignas(8) uint64_t bar_words[2 * S::kStagesW + 2 * COPIES + 2 * S::kStagesA + 1];
   __shared__ uint32_t tmem_word;
   __shared__ int dead_word;
-  __shared__ float token_scale[BN];
+  __shared__ float token_scale[BN], channel_scale[128];
   volatile int* const dead = &dead_word;
   const uint32_t ring = (smem_addr(raw_smem) + 1023u) & ~1023u;
   const uint32_t w_full = smem_addr(bar_words), w_empty = w_full + 8 * S::kStagesW;
@@ -381,9 +434,7 @@ __global__ void __launch_bounds__(Stream<CTAS, BN, RAW>::kThreads,
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const uint32_t tmem = tmem_word, tmem_a = tmem + BN;
   const int group = (warp - 4) / 4, quarter = warp % 4;   // of warps 4 to 11
-  const long long i = (long long)row_w + quarter * 32 + lane;   // this thread's channel
   const long long j0 = (long long)tn * BN;
-  float channel = 0.f;
   bool ok = true;
 
   if (warp < 2 && lane == 0) {
@@ -454,7 +505,6 @@ __global__ void __launch_bounds__(Stream<CTAS, BN, RAW>::kThreads,
     // one before it.
     const int row = quarter * 32 + lane;
     const uint32_t lead_full = CTAS == 2 ? cluster_address(a_full, 0) : a_full;
-    if (i < a.m) channel = a.sw != nullptr ? a.sw[i] : 1.f;
     for (int u = 0; u < mine; ++u) {
       const int stage = u % S::kStagesW, sa = u % S::kStagesA;
       ok = wait_or_dead(w_full + 8 * stage, u / S::kStagesW & 1, dead, limit_ns);
@@ -542,88 +592,74 @@ __global__ void __launch_bounds__(Stream<CTAS, BN, RAW>::kThreads,
       if (lane == 0) mbar_arrive(a_full + 8 * sa);
     }
   } else if (warp == 3) {
+#pragma unroll 1
     for (int c = lane; c < BN; c += 32)
       token_scale[c] = j0 + c < a.n ? token_factor(a, j0 + c) : 0.f;
+#pragma unroll 1
+    for (int c = lane; c < 128; c += 32)
+      channel_scale[c] = row_w + c < a.m && a.sw != nullptr ? a.sw[row_w + c] : 1.f;
   }
   // a warp's failure is the CTA's: its results are NaN
   __syncwarp();
   if (!ok) *dead = 1;
-  const float nan = __uint_as_float(0x7fc00000u);
   if (split == 1) {
     __syncthreads();
     tensor_fence_after();
-    const bool good = *dead == 0;
-    if (warp >= 4 && warp < 12)
-      for (int c0 = group * 16; c0 < BN && j0 + c0 < a.n; c0 += 32) {
-        uint32_t r[16];
-        tmem_load16(r, tmem + ((uint32_t)(quarter * 32) << 16) + c0);
-        float v[16];
-#pragma unroll
-        for (int c = 0; c < 16; ++c) v[c] = good ? __uint_as_float(r[c]) : nan;
-        if (i < a.m)
-          store_tokens_any(a, i, j0 + c0, (int)min(16LL, a.n - j0 - c0), v, channel,
-                           token_scale + c0);
-        __syncwarp();
-      }
-    if (CTAS == 2) {
-      tensor_fence_before();
-      cluster_sync();
+    if (warp >= 4 && warp < 12) {
+      const int at = quarter * 32 + lane;
+      const long long i = (long long)row_w + at;
+      const float channel = *dead != 0 ? __uint_as_float(0x7fc00000u) : channel_scale[at];
+      const uint32_t from = tmem + ((uint32_t)(quarter * 32) << 16);
+      if (a.type == 's')
+        store_columns<float>(a, from, i, j0, group * 16, 32, BN, channel, token_scale);
+      else if (a.type == 'h')
+        store_columns<__half>(a, from, i, j0, group * 16, 32, BN, channel, token_scale);
+      else
+        store_columns<__nv_bfloat16>(a, from, i, j0, group * 16, 32, BN, channel, token_scale);
     }
+    tensor_fence_before();
+    if (CTAS == 2)
+      cluster_sync();
+    else
+      __syncthreads();
   } else {
-    // CTA q of the cluster adds columns q*width .. of all: [rank][column / 4][channel][column % 4]
-    // in its shared memory, which every CTA has finished with
+    // the accumulators' columns q*width .. to CTA q of the cluster, into the shared memory
+    // that every CTA has finished with
     cluster_sync();
     tensor_fence_after();
-    const int width = BN / split, chunk = min(width, 4);   // 2, 4 or more
-    const bool good = *dead == 0;
-    if (warp >= 4 && warp < 12)
+    const int width = BN / split;
+    if (warp >= 4 && warp < 12) {
+      const bool good = *dead == 0;
+#pragma unroll 1
       for (int c0 = group * 16; c0 < BN; c0 += 32) {
         uint32_t r[16];
         tmem_load16(r, tmem + ((uint32_t)(quarter * 32) << 16) + c0);
-        if (!good)
-#pragma unroll
-          for (int c = 0; c < 16; ++c) r[c] = 0x7fc00000u;
 #pragma unroll
         for (int c = 0; c < 16; c += 4) {
-          const int owner = (c0 + c) / width, col = (c0 + c) - owner * width;
-          const uint32_t slot = (uint32_t)(rank * width + col) * 512u +
-                                (uint32_t)(quarter * 32 + lane) * 4u * chunk;
-          if (chunk == 4) {
-            cluster_store4(cluster_address(ring, owner) + slot, r[c], r[c + 1], r[c + 2], r[c + 3]);
-          } else {
-            cluster_store2(cluster_address(ring, owner) + slot, r[c], r[c + 1]);
-            cluster_store2(cluster_address(ring, owner + 1) + slot, r[c + 2], r[c + 3]);
-          }
+          const int owner = (c0 + c) / width, col = c0 + c - owner * width;
+          const uint32_t slot =
+              ring + (uint32_t)((rank * width + col) * 128 + (quarter * 32 + lane) * 4) * 4u;
+          if (!good) r[c] = r[c + 1] = r[c + 2] = r[c + 3] = 0x7fc00000u;
+          cluster_store4(cluster_address(slot, owner), r[c], r[c + 1], r[c + 2], r[c + 3]);
         }
       }
+      tensor_fence_before();
+    }
     cluster_sync();
-    if (warp >= 4 && warp < 12)
-      for (int c = group * chunk; c < width; c += 2 * chunk) {
-        const int col = rank * width + c;
-        float v[16];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          v[e] = 0.f;
-          if (e < chunk)
-            for (int r = 0; r < split; ++r) {
-              float p;
-              asm volatile("ld.shared.f32 %0, [%1];"
-                           : "=f"(p)
-                           : "r"(ring + (r * width + c) * 512 +
-                                 ((quarter * 32 + lane) * chunk + e) * 4)
-                           : "memory");
-              v[e] += p;
-            }
-        }
-        if (j0 + col < a.n && i < a.m)
-          store_tokens_any(a, i, j0 + col, (int)min((long long)chunk, a.n - j0 - col), v, channel,
-                           token_scale + col);
-      }
+    const long long j = j0 + rank * width;
+    const TileResult t{ring, split, width, row_w, j, channel_scale, token_scale + rank * width,
+                       *dead != 0};
+    if (a.type == 's')
+      store_result<float, 1>(a, t, S::kThreads);
+    else if (((reinterpret_cast<uintptr_t>(a.Y) | (uintptr_t)a.ldy * 2) & 3) != 0)
+      a.type == 'h' ? store_result<__half, 1>(a, t, S::kThreads)
+                    : store_result<__nv_bfloat16, 1>(a, t, S::kThreads);
+    else
+      a.type == 'h' ? store_result<__half, 2>(a, t, S::kThreads)
+                    : store_result<__nv_bfloat16, 2>(a, t, S::kThreads);
   }
   if (*dead != 0 && threadIdx.x == 0) atomicMax(status, epoch);
   __syncwarp();
-  tensor_fence_before();
-  __syncthreads();
   tensor_fence_after();
   if (warp == 3) tmem_free<CTAS>(tmem, S::kColumns);
 }

@@ -36,15 +36,12 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
-// 16 or 8 bytes to the shared memory of another CTA of the cluster
+// 16 bytes to the shared memory of another CTA of the cluster
 __device__ __forceinline__ void cluster_store4(uint32_t to, uint32_t a, uint32_t b, uint32_t c,
                                                uint32_t d) {
   asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(a), "r"(b),
                "r"(c), "r"(d)
                : "memory");
-}
-__device__ __forceinline__ void cluster_store2(uint32_t to, uint32_t a, uint32_t b) {
-  asm volatile("st.shared::cluster.v2.b32 [%0], {%1, %2};" ::"r"(to), "r"(a), "r"(b) : "memory");
 }
 
 // All lanes' reads of shared memory so far have returned.  Without the fence an
