@@ -64,18 +64,29 @@ __device__ __forceinline__ void halves_of(uint32_t q, uint32_t& lo, uint32_t& hi
 
 // ---------------------------------------------------------- a few tokens --
 
+// Loads of what the predecessor may still be writing when this kernel begins, so not
+// through the path for data that is constant while a kernel runs.
+__device__ __forceinline__ uint4 load_once(const void* p) {   // not kept in L1
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ uint4 load_shared_use(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p)
+               : "memory");
+  return v;
+}
 // 16 integers first .. first+15 of the k of `row` (first a multiple of 16), at any
 // alignment.  GRID: rows start on 16-byte boundaries and are multiples of 16
 // long.  MASK: those beyond k are zero; else they are any integers (their
 // partners are zero).  Only 16-byte pieces that hold an element of the row are
 // read.
-__device__ __forceinline__ uint4 load_once(const void* p) {
-  uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p));
-  return v;
-}
 template <bool GRID, bool MASK>
 __device__ __forceinline__ uint4 load16(const int8_t* row, int first, int k) {
   uint4 z = make_uint4(0, 0, 0, 0);
@@ -83,7 +94,7 @@ __device__ __forceinline__ uint4 load16(const int8_t* row, int first, int k) {
   const int8_t* at = row + first;
   // X is read by many warps, W once (but off the grid a piece of it by two lanes)
   auto piece = [](const void* p) {
-    return MASK || !GRID ? __ldg(reinterpret_cast<const uint4*>(p)) : load_once(p);
+    return MASK || !GRID ? load_shared_use(p) : load_once(p);
   };
   if (GRID) return piece(at);
   const unsigned off = (unsigned)(reinterpret_cast<uintptr_t>(at) % 16);

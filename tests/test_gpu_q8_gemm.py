@@ -234,3 +234,85 @@ def test_norm_feeds_product(kind):
         worst = (hn.abs().amax(1)[:, None] * wt.double().abs().sum(1)[None, :]
                  + hn.abs().sum(1)[:, None] * wt.double().abs().amax(1)[None, :]) / 254 * 1.01
         assert bool(((y.double() - full).abs() <= worst + UNIT[kind] * full.abs() + 1e-3).all())
+
+
+@pytest.mark.parametrize("n", [1, 5, 8, 20, 33, 64, 90, 300])
+def test_queued_layers_see_their_own_activations(n):
+    """norms and products queued behind one another through the same 8-bit buffers:
+    every product reads what the norm before it wrote, not what was there earlier"""
+    m, k, layers = 512, 1024, 24
+    g = gen(n)
+    w = integers(g, m, k)
+    xs_in = torch.randn((layers, n, k), generator=g, device="cuda").bfloat16()
+    q = torch.empty((n, k), dtype=torch.int8, device="cuda")
+    s = torch.empty((n,), device="cuda")
+    y = torch.empty((layers, n, m), device="cuda")
+    qs, ss = torch.empty((layers, n, k), dtype=torch.int8, device="cuda"), torch.empty((layers, n), device="cuda")
+    for i in range(layers):        # each alone
+        assert xs.rmsquant("b", k, n, xs_in[i], k, None, 0, None, 1e-5, None, 0, qs[i], k, ss[i], None) == 0
+        torch.cuda.synchronize()
+    want = torch.stack([(qs[i].double() @ w.double().T) * ss[i].double()[:, None] for i in range(layers)])
+    for _ in range(20):
+        y.fill_(float("nan"))
+        for i in range(layers):    # queued
+            assert xs.rmsquant("b", k, n, xs_in[i], k, None, 0, None, 1e-5, None, 0, q, k, s, None) == 0
+            assert xs.gemmq("s", m, n, k, 1.0, w, k, None, q, k, s, 0.0, y[i], m) == 0
+        torch.cuda.synchronize()
+        assert bool(((y.double() - want).abs() <= 4 * ref.U32 * want.abs()).all())
+
+
+@pytest.mark.parametrize("n", [1, 20, 100])
+def test_queued_weights(n):
+    """the weights written by the kernel just before the product: every product reads
+    its own, equal to those that the same call gives alone"""
+    m, k = 512, 1024
+    g = gen(n)
+    x = integers(g, n, k)
+    ws = torch.randn((12, m, k), generator=g, device="cuda").half()
+    w = torch.empty((m, k), dtype=torch.int8, device="cuda")
+    sw = torch.empty((m,), device="cuda")
+    y = torch.empty((12, n, m), device="cuda")
+    want = []
+    for i in range(12):
+        assert xs.quant("h", k, m, ws[i], k, w, k, sw) == 0
+        torch.cuda.synchronize()
+        want.append((x.double() @ w.double().T) * sw.double())
+    want = torch.stack(want)
+    for _ in range(10):
+        for i in range(12):
+            assert xs.quant("h", k, m, ws[i], k, w, k, sw) == 0
+            assert xs.gemmq("s", m, n, k, 1.0, w, k, sw, x, k, None, 0.0, y[i], m) == 0
+        torch.cuda.synchronize()
+        assert bool(((y.double() - want).abs() <= 4 * ref.U32 * want.abs()).all())
+
+
+@pytest.mark.parametrize("m,n,k", [(700, 20, 640), (700, 64, 640), (700, 100, 640), (130, 50, 64),
+                                   (2048, 2048, 256)])
+def test_waits_that_run_out(m, n, k):
+    """copies whose barrier expects bytes that never arrive (nothing faults): the
+    kernel returns after the limit, Y is NaN, the status says so, and the next
+    call is right"""
+    g = gen(n)
+    w, x = integers(g, m, k), integers(g, n, k)
+    y = torch.zeros((n, m), device="cuda")
+
+    def run():
+        st = xs.gemmq("s", m, n, k, 1.0, w, k, None, x, k, None, 0.0, y, m)
+        assert st == 0
+        return xs.xsymv_sync_status()
+
+    want = x.double() @ w.double().T
+    assert run() == 0 and torch.equal(y.double(), want)
+    xs.xsymv_set_wait_limit(2_000_000)
+    try:
+        xs.xsymv_test_stall(True)
+        assert run() == -6
+        assert bool(torch.isnan(y).all())
+        xs.xsymv_test_stall(False)
+        assert run() == 0 and torch.equal(y.double(), want)
+    finally:
+        xs.xsymv_test_stall(False)
+        xs.xsymv_set_wait_limit(0)
+    # a call without such waits reports none
+    s = torch.empty((1,), device="cuda")
+    assert xs.quant("s", 4, 1, y, 4, w, 4, s) == 0 and xs.xsymv_sync_status() == 0
