@@ -219,7 +219,9 @@ int gemmq_entry(char type, int m, int n, int k, float alpha, const int8_t* W, in
   }
   if (n <= kFewTokens && k <= kFewMostDepth) {
     const bool g = k % 16 == 0 && on_grid(W, ldw) && on_grid(X, ldx);
-    const long long blocks = (m + kMmaRows - 1LL) / kMmaRows;
+    // off the grid a block's rows lie 16 apart, and every alignment has its blocks
+    const long long blocks = g ? (m + kMmaRows - 1LL) / kMmaRows
+                               : (m + 16LL * kMmaRows - 1) / (16 * kMmaRows) * 16;
     const int split = depth_split(blocks, (k + kFewStep - 1) / kFewStep, 4LL * sms);
     return launched(launch_cluster(g ? gemmq_few<true> : gemmq_few<false>,
                                    (unsigned)(blocks * split), split, kMmaWarps * 32, 0, true, st,

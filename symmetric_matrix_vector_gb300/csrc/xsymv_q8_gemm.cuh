@@ -82,38 +82,31 @@ __device__ __forceinline__ uint4 load_shared_use(const void* p) {
                : "memory");
   return v;
 }
-// 16 integers first .. first+15 of the k of `row` (first a multiple of 16), at any
-// alignment.  GRID: rows start on 16-byte boundaries and are multiples of 16
-// long.  MASK: those beyond k are zero; else they are any integers (their
-// partners are zero).  Only 16-byte pieces that hold an element of the row are
-// read.
-template <bool GRID, bool MASK>
+// 16 integers first .. first+15 of the k of `row`, zeros outside 0 .. k-1, at any
+// alignment.  GRID: rows start on 16-byte boundaries, first and k are multiples of 16.
+// Only 16-byte pieces that hold an element of the row are read.
+template <bool GRID>
 __device__ __forceinline__ uint4 load16(const int8_t* row, int first, int k) {
   uint4 z = make_uint4(0, 0, 0, 0);
-  if (first >= k) return z;
+  if (first >= k || (!GRID && first <= -16)) return z;
   const int8_t* at = row + first;
-  // X is read by many warps, W once (but off the grid a piece of it by two lanes)
-  auto piece = [](const void* p) {
-    return MASK || !GRID ? load_shared_use(p) : load_once(p);
-  };
-  if (GRID) return piece(at);
+  if (GRID) return load_shared_use(at);
   const unsigned off = (unsigned)(reinterpret_cast<uintptr_t>(at) % 16);
-  const uint4 a = piece(at - off);
-  if (off == 0) {
-    z = a;
-  } else {
-    uint4 b = z;
-    if (at - off + 16 < row + k) b = piece(at - off + 16);
-    uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-    shift_words<4>(w, off);
-    const unsigned bits = (off & 3) * 8;
-    z = make_uint4(__funnelshift_r(w[0], w[1], bits), __funnelshift_r(w[1], w[2], bits),
-                   __funnelshift_r(w[2], w[3], bits), __funnelshift_r(w[3], w[4], bits));
-  }
-  if (MASK && first + 16 > k) {
-    const int left = k - first;   // 1 .. 15
+  uint4 a = z, b = z;
+  if (at - off + 16 > row) a = load_shared_use(at - off);
+  if (off != 0 && at - off + 16 < row + k) b = load_shared_use(at - off + 16);
+  uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  shift_words<4>(w, off);
+  const unsigned bits = (off & 3) * 8;
+  z = make_uint4(__funnelshift_r(w[0], w[1], bits), __funnelshift_r(w[1], w[2], bits),
+                 __funnelshift_r(w[2], w[3], bits), __funnelshift_r(w[3], w[4], bits));
+  if (first + 16 > k || first < 0) {
+    // bytes lo .. hi-1 of the 16 are the row's
+    const int lo = max(0, -first), hi = min(16, k - first);
     auto keep = [&](uint32_t v, int at) {
-      return left >= at + 4 ? v : left <= at ? 0u : v & ((1u << 8 * (left - at)) - 1u);
+      if (hi < at + 4) v = hi <= at ? 0u : v & ((1u << 8 * (hi - at)) - 1u);
+      if (lo > at) v = lo >= at + 4 ? 0u : v & (~0u << 8 * (lo - at));
+      return v;
     };
     z = make_uint4(keep(z.x, 0), keep(z.y, 4), keep(z.z, 8), keep(z.w, 12));
   }
@@ -127,6 +120,12 @@ __device__ __forceinline__ uint4 load16(const int8_t* row, int first, int k) {
 // its 8 warps take every 8th 64 of its part of the depth and add their sums in shared
 // memory, in warp order, then the CTAs of a cluster (as many as share the depth
 // where there are few rows) theirs in rank 0's, in rank order.
+//
+// Off the 16-byte grid (GRID false) a block takes rows 16 apart: whatever ldw is,
+// they all lie `skew` bytes beyond a boundary, so W is read in aligned pieces and
+// only X, from L1, is shifted to meet them: element p of the shifted depth is
+// element p - skew of X, zero outside it (32768 x 8193, one token: 106 us with W
+// shifted, 49 us so).
 constexpr int kFewTokens = 8, kFewMostDepth = 1 << 22;
 constexpr int kMmaWarps = 8, kMmaRows = 32, kFewStep = kMmaWarps * 64;
 __device__ __forceinline__ void mma_16x8x16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
@@ -142,17 +141,26 @@ __global__ void __launch_bounds__(kMmaWarps * 32, 4) gemmq_few(GemmqArgs a, int 
   __shared__ float buf[kMmaWarps][kMmaRows][kFewTokens + 2];
   __shared__ float parts[8][kFewTokens][kMmaRows];   // of the cluster's CTAs
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
-  const int rank = split > 1 ? (int)cluster_rank() : 0;
-  const long long i0 = (long long)(blockIdx.x / split) * kMmaRows;
+  const int rank = split > 1 ? (int)cluster_rank() : 0, tile = blockIdx.x / split;
+  // rows i0 + j * kApart of the tile, j < rows
+  constexpr int kApart = GRID ? 1 : 16;
+  const long long i0 = GRID ? (long long)tile * kMmaRows
+                            : (long long)(tile / kApart) * kApart * kMmaRows + tile % kApart;
+  const int rows = (int)max(0LL, min((long long)kMmaRows, (a.m - i0 + kApart - 1) / kApart));
+  const int skew =
+      GRID ? 0 : (int)(reinterpret_cast<uintptr_t>(a.W + min(i0, a.m - 1LL) * a.ldw) % 16);
   // rows g, g + 8, .. of the tile; for those beyond the last row, another one
-  const int8_t* const w0 = a.W + min(i0 + g, a.m - 1LL) * a.ldw;
-  const int left = (int)min((long long)kMmaRows, a.m - i0) - g;
-  const long long down = 8 * a.ldw;
-  auto row = [&](int r) { return 8 * r < left ? w0 + r * down : w0; };
+  const int8_t* const w0 =
+      a.W + min(i0 + (long long)min(g, max(rows, 1) - 1) * kApart, a.m - 1LL) * a.ldw - skew;
+  const long long down = 8LL * kApart * a.ldw;
+  auto row = [&](int r) { return g + 8 * r < rows ? w0 + r * down : w0; };
+  auto load_w = [&](int r, int p, int end) {
+    return p < end ? load_once(row(r) + p) : make_uint4(0, 0, 0, 0);
+  };
   const int8_t* const x = a.X + min(g, a.n - 1) * a.ldx;
   // this CTA's part of the depth: whole steps of the block
-  const int steps = (a.k + kFewStep - 1) / kFewStep;
-  const int end = min(a.k, (int)((long long)steps * (rank + 1) / split) * kFewStep);
+  const int depth = a.k + skew, steps = (depth + kFewStep - 1) / kFewStep;
+  const int end = min(depth, (int)((long long)steps * (rank + 1) / split) * kFewStep);
   int p = (int)((long long)steps * rank / split) * kFewStep + warp * 64 + t * 16;
   // its first integers of W on their way to L2 while the predecessor still runs
 #pragma unroll
@@ -166,15 +174,15 @@ __global__ void __launch_bounds__(kMmaWarps * 32, 4) gemmq_few(GemmqArgs a, int 
     for (int e = 0; e < 4; ++e) acc[h][e] = 0.f;
   uint4 next[4];
 #pragma unroll
-  for (int r = 0; r < 4; ++r) next[r] = load16<GRID, false>(row(r), p, end);
+  for (int r = 0; r < 4; ++r) next[r] = load_w(r, p, end);
   for (; p - t * 16 < end; p += kFewStep) {
     uint4 q[4];
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       q[r] = next[r];
-      next[r] = load16<GRID, false>(row(r), p + kFewStep, end);
+      next[r] = load_w(r, p + kFewStep, end);
     }
-    const uint4 v = load16<GRID, true>(x, p, end);
+    const uint4 v = p < end ? load16<GRID>(x, p - skew, a.k) : make_uint4(0, 0, 0, 0);
 #pragma unroll
     for (int s = 0; s < 4; ++s) {   // 4 of the lane's 16 integers
       auto word = [s](const uint4& u) { return s == 0 ? u.x : s == 1 ? u.y : s == 2 ? u.z : u.w; };
@@ -206,7 +214,7 @@ __global__ void __launch_bounds__(kMmaWarps * 32, 4) gemmq_few(GemmqArgs a, int 
     v = 0.f;
     for (int r = 0; r < split; ++r) v += parts[r][warp][lane];
   }
-  if (warp < a.n && i0 + lane < a.m) store_any(a, i0 + lane, warp, v);
+  if (warp < a.n && lane < rows) store_any(a, i0 + (long long)lane * kApart, warp, v);
 }
 
 // ------------------------------------------------ operands made beforehand --
@@ -241,7 +249,7 @@ __global__ void __launch_bounds__(256) prepare_kernel(Prepare a, Prepare b, int 
     for (int u = 0; u < U; ++u) {
       const long long at = p + (long long)u * c.along * 16;
       if (at < c.width)
-        v[u] = c.grid ? load16<true, true>(q, (int)at, c.k) : load16<false, true>(q, (int)at, c.k);
+        v[u] = c.grid ? load16<true>(q, (int)at, c.k) : load16<false>(q, (int)at, c.k);
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
