@@ -1,0 +1,105 @@
+"""A linear layer in 8 bits, as a serving step and as a training step use it.
+
+    python -m symmetric_matrix_vector_gb300.q8_layer [channels] [width] [tokens]
+
+``Q8Linear`` keeps a weight in 8 bits with a scale for each output channel.
+Serving: the residual is added and normalised straight to 8 bits (rmsquant) and
+multiplied with the weight (gemmq), for a prompt or for a single token alike.
+Training with the quantiser in the loop: the values that the 8-bit activations
+and weights stand for (dequant) go through ordinary 16-bit products, and the
+gradient of the norm (rmsgrad) passes straight through the rounding.
+
+Tensors are row-major with one token (or one output channel) a row: the
+library's column-major storage with one token a column.
+"""
+from __future__ import annotations
+
+import sys
+
+import torch
+
+import symmetric_matrix_vector_gb300 as xs
+
+KIND = {torch.float32: "s", torch.float16: "h", torch.bfloat16: "b"}
+
+
+class Q8Linear:
+    """y = norm(x + residual) @ weight.T with the norm's output and the weight in
+    8 bits.  weight: (channels, width), norm_weight: (width,), one type."""
+
+    def __init__(self, weight: torch.Tensor, norm_weight: torch.Tensor, eps: float = 1e-5):
+        self.channels, self.width = weight.shape
+        self.kind, self.eps, self.g = KIND[weight.dtype], eps, norm_weight
+        self.w = torch.empty((self.channels, self.width), dtype=torch.int8, device=weight.device)
+        self.sw = torch.empty((self.channels,), device=weight.device)
+        xs.check(xs.quant(self.kind, self.width, self.channels, weight, weight.stride(0), self.w,
+                          self.width, self.sw))
+
+    def norm(self, x, residual):
+        """(h, q, scale, rstd): the new residual, and its norm in 8 bits"""
+        n, k = x.shape[0], self.width
+        h = torch.empty_like(residual)
+        q = torch.empty((n, k), dtype=torch.int8, device=x.device)
+        scale, rstd = torch.empty((2, n), device=x.device)
+        xs.check(xs.rmsquant(self.kind, k, n, x, x.stride(0), residual, residual.stride(0), self.g,
+                             self.eps, h, h.stride(0), q, k, scale, rstd))
+        return h, q, scale, rstd
+
+    def forward(self, x, residual):
+        """(y, h): a serving step for the rows (tokens) of x"""
+        h, q, scale, _ = self.norm(x, residual)
+        y = torch.empty((x.shape[0], self.channels), dtype=x.dtype, device=x.device)
+        xs.check(xs.gemmq(self.kind, self.channels, x.shape[0], self.width, 1.0, self.w, self.width,
+                          self.sw, q, self.width, scale, 0.0, y, self.channels))
+        return y, h
+
+    def train_step(self, x, residual, dy, dh):
+        """Forward and backward of one step: dy the gradient of the layer's output, dh
+        that of the new residual.  Returns (y, gradient of x and of the residual,
+        gradient of the norm's weight, gradient of the weight)."""
+        n, k = x.shape[0], self.width
+        h, q, scale, rstd = self.norm(x, residual)
+        a = torch.empty_like(h)                      # what the 8-bit values stand for
+        w = torch.empty((self.channels, k), dtype=x.dtype, device=x.device)
+        xs.check(xs.dequant(self.kind, k, n, q, k, scale, a, k))
+        xs.check(xs.dequant(self.kind, k, self.channels, self.w, k, self.sw, w, k))
+        y = a @ w.T
+        da, dw = dy @ w, dy.T @ a
+        dx = torch.empty_like(h)
+        dg = torch.empty((k,), device=x.device)
+        xs.check(xs.rmsgrad(self.kind, k, n, da, k, h, k, self.g, rstd, dh, dh.stride(0), dx, k, dg))
+        return y, dx, dg, dw
+
+
+def main(channels: int = 4096, width: int = 4096, tokens: int = 300) -> None:
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(0)
+
+    def normal(*shape, scale=1.0):
+        return (torch.randn(shape, generator=gen, device="cuda") * scale).to(torch.bfloat16)
+
+    weight, g = normal(channels, width, scale=0.02), 1 + normal(width, scale=0.1)
+    layer = Q8Linear(weight, g)
+    x, residual = normal(tokens, width), normal(tokens, width)
+
+    def plain(x, residual):
+        h = x.float() + residual.float()
+        u = h * torch.rsqrt(h.square().mean(1, keepdim=True) + layer.eps) * g.float()
+        return u @ weight.float().T
+
+    y, h = layer.forward(x, residual)
+    off = (y.float() - plain(x, residual)).norm() / plain(x, residual).norm()
+    print("prompt of %d tokens: output within %.2g of the unquantised layer" % (tokens, off))
+    for t in range(3):                               # single tokens, as a decoder makes them
+        one, res = normal(1, width), h[-1:].clone()
+        y1, h1 = layer.forward(one, res)
+        ref = plain(one, res)
+        print("token %d: within %.2g" % (t, (y1.float() - ref).norm() / ref.norm()))
+    y, dx, dg, dw = layer.train_step(x, residual, normal(tokens, channels), normal(tokens, width))
+    print("training step: gradients of the residual %s, norm weight %s, weight %s"
+          % (tuple(dx.shape), tuple(dg.shape), tuple(dw.shape)))
+    print("kernel launches: %d" % xs.xsymv_launch_count())
+
+
+if __name__ == "__main__":
+    main(*(int(v) for v in sys.argv[1:4]))
