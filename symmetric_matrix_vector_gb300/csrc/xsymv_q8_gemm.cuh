@@ -535,8 +535,6 @@ __global__ void __launch_bounds__(Stream<CTAS, BN, RAW>::kThreads,
       uint4 q[4];
 #pragma unroll
       for (int c = 0; c < 4; ++c) q[c] = lds128(at + (((4 * group + c) ^ (row & 7)) << 4));
-      reads_done();
-      if (lane == 0) mbar_arrive(w_empty + 8 * stage);
       ok = wait_or_dead(a_empty + 8 * sa, (u / S::kStagesA & 1) ^ 1, dead, limit_ns);
       if (!__all_sync(0xffffffffu, ok)) {
         ok = false;
@@ -561,6 +559,11 @@ __global__ void __launch_bounds__(Stream<CTAS, BN, RAW>::kThreads,
       tensor_fence_before();
       __syncwarp();
       if (lane == 0) {
+        // the stage goes back to the copies only now that its integers have reached
+        // tensor memory: an arrival right after the loads, even behind a fence, can
+        // overtake loads on their way (once in some 60 000 calls a row of W was that of
+        // a later step)
+        mbar_arrive(w_empty + 8 * stage);
         if (CTAS == 2)
           mbar_arrive_cluster(lead_full + 8 * sa);
         else
@@ -586,8 +589,6 @@ __global__ void __launch_bounds__(Stream<CTAS, BN, RAW>::kThreads,
         const int r = id / 8 + 16 * e, c = id % 8;
         q[e] = lds128(ring + S::kAtRaw + stage * S::kBytesRaw + r * 128 + ((c ^ (r & 7)) << 4));
       }
-      reads_done();
-      if (lane == 0) mbar_arrive(x_empty + 8 * stage);
       ok = wait_or_dead(a_empty + 8 * sa, (u / S::kStagesA & 1) ^ 1, dead, limit_ns);
       if (!__all_sync(0xffffffffu, ok)) {
         ok = false;
@@ -608,7 +609,10 @@ __global__ void __launch_bounds__(Stream<CTAS, BN, RAW>::kThreads,
       // what the tensor cores read, which see shared memory as copies do
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
-      if (lane == 0) mbar_arrive(a_full + 8 * sa);
+      if (lane == 0) {
+        mbar_arrive(x_empty + 8 * stage);   // all of it has been stored as halves
+        mbar_arrive(a_full + 8 * sa);
+      }
     }
   } else if (warp == 3) {
 #pragma unroll 1

@@ -44,14 +44,6 @@ __device__ __forceinline__ void cluster_store4(uint32_t to, uint32_t a, uint32_t
                : "memory");
 }
 
-// All lanes' reads of shared memory so far have returned.  Without the fence an
-// arrival that hands the memory back to a copy can overtake loads on their way
-// (seen: a row, or 32, of the tile after next, once in some hundred calls).
-__device__ __forceinline__ void reads_done() {
-  __threadfence_block();
-  __syncwarp();
-}
-
 // Wait for phase `parity`, giving up once `limit_ns` have passed or another
 // wait of this CTA has given up (*dead).  A wait that gives up sets *dead.
 __device__ __forceinline__ bool wait_or_dead(uint32_t bar, uint32_t parity, volatile int* dead,
