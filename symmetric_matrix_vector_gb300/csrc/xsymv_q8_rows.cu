@@ -441,10 +441,17 @@ struct Slot {
       const char* at = reinterpret_cast<const char*>(row + first) - o;
 #pragma unroll
       for (int k = 0; k < PIECES; ++k)
-        if (k < N / 4 || o != 0)
-          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(slot + k * apart),
-                       "l"(at + 16 * k)
-                       : "memory");
+        if (k < N / 4 || o != 0) {
+          // where two requests share every 32-byte sector they meet in L1
+          if (GRID && PIECES == 1)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(slot + k * apart),
+                         "l"(at + 16 * k)
+                         : "memory");
+          else
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(slot + k * apart),
+                         "l"(at + 16 * k)
+                         : "memory");
+        }
     } else {
       const Raw<T> r = load8<false>(row, first, m);
 #pragma unroll
@@ -485,7 +492,8 @@ template <class T, int KNV, bool GRID>
 constexpr int kGradSlots = kGradOperands * KNV * Slot<T, GRID>::PIECES;
 
 template <class T, int KNV, bool GRID>
-__global__ void __launch_bounds__(512) rmsgrad_kernel(RmsgradArgs<T> a, int stages) {
+__global__ void __launch_bounds__(512, GRID && KNV <= 2 ? 2 : 1)
+    rmsgrad_kernel(RmsgradArgs<T> a, int stages) {
   using S = Slot<T, GRID>;
   extern __shared__ uint4 slots[];
   __shared__ float2 buf[2][kWarps];
@@ -637,10 +645,10 @@ __global__ void __launch_bounds__(1024) rmsgrad_long_kernel(RmsgradArgs<T> a) {
 
 // ... and their dG, before dX may overwrite dY or H: block (x, y) sums 32 packs
 // of rows of dG over the y-th share of the columns
-constexpr int kTall = 16;
+constexpr int kDeepRows = 16, kTall = 32;
 template <class T>
-__global__ void __launch_bounds__(32 * kTall) rmsgrad_weight_kernel(RmsgradArgs<T> a, int share) {
-  __shared__ float buf[kTall][32 * kPack + 1];
+__global__ void __launch_bounds__(32 * kDeepRows) rmsgrad_weight_kernel(RmsgradArgs<T> a, int share) {
+  __shared__ float buf[kDeepRows][32 * kPack + 1];
   await_predecessor();
   const int first = ((int)blockIdx.x * 32 + (int)threadIdx.x) * kPack;
   const long long end = min((long long)a.n, (blockIdx.y + 1LL) * share);
@@ -648,7 +656,7 @@ __global__ void __launch_bounds__(32 * kTall) rmsgrad_weight_kernel(RmsgradArgs<
 #pragma unroll
   for (int k = 0; k < kPack / 2; ++k) s[k] = make_float2(0.f, 0.f);
 #pragma unroll 2
-  for (long long j = (long long)blockIdx.y * share + threadIdx.y; j < end; j += kTall) {
+  for (long long j = (long long)blockIdx.y * share + threadIdx.y; j < end; j += kDeepRows) {
     const float rstd = a.rstd[j];
     const Floats d = floats_of(load8<false>(a.dY + j * a.lddy, first, a.m));
     const Floats u = floats_of(load8<false>(a.H + j * a.ldh, first, a.m));
@@ -666,27 +674,29 @@ __global__ void __launch_bounds__(32 * kTall) rmsgrad_weight_kernel(RmsgradArgs<
   if (at < 32 * kPack && i < a.m) {
     float t = 0.f;
 #pragma unroll
-    for (int y = 0; y < kTall; ++y) t += buf[y][at];
+    for (int y = 0; y < kDeepRows; ++y) t += buf[y][at];
     a.parts[(long long)blockIdx.y * a.m + i] = t;
   }
 }
 
 // dG = the sum of the `count` partial sums, m apart (count = 0: zero)
-__global__ void weight_sum_kernel(int m, int count, const float* parts, float* dG) {
+__global__ void __launch_bounds__(32 * kTall) weight_sum_kernel(int m, int count,
+                                                                const float* parts, float* dG) {
   __shared__ float buf[kTall][33];
   await_predecessor();
   const int i = blockIdx.x * 32 + threadIdx.x;
   float s = 0.f;
   if (i < m)
-#pragma unroll 4
+#pragma unroll 8
     for (int c = threadIdx.y; c < count; c += kTall) s += parts[(long long)c * m + i];
   buf[threadIdx.y][threadIdx.x] = s;
   __syncthreads();
-  if (threadIdx.y == 0 && i < m) {
+  // a warp a row, lanes along its partial sums
+  s = buf[threadIdx.x][threadIdx.y];
 #pragma unroll
-    for (int y = 1; y < kTall; ++y) s += buf[y][threadIdx.x];
-    dG[i] = s;
-  }
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  const int at = blockIdx.x * 32 + threadIdx.y;
+  if (threadIdx.x == 0 && at < m) dG[at] = s;
 }
 
 // ------------------------------------------------------------------- host --
@@ -837,17 +847,22 @@ int rmsgrad_entry(int m, int n, const T* dY, int lddy, const T* H, int ldh, cons
   int dev, sms;
   if (!current_device(&dev, &sms)) return XSYMV_ERR_DEVICE;
   cudaStream_t st = current_stream();
-  Shape s = shape_for<T>(m, n, 0, 512);
   const bool g = m % kPack == 0 && most_head(dY, lddy) == 0 && most_head(H, ldh) == 0 &&
                  most_head(G, 0) == 0 && (dR == nullptr || most_head(dR, lddr) == 0) &&
                  most_head(dX, lddx) == 0;
+  // On the grid few packs a thread, so that two blocks of 512 threads fit on an SM
+  // (4096 x 16384 halves: 1 pack 86 us, 4 packs in blocks of 128 threads 90); off it, where
+  // a pack takes twice the registers, small blocks (4099 x 8192: 104 us against 146)
+  Shape s = shape_for<T>(m, g ? 1 : n, 0, 512);
   const GradKernel<T> kernel = grad_kernel<T>(s.packs, g);
   const long long stage_bytes = (long long)kernel.slots * 16 * s.threads;
   if (stage_bytes > kSmemPerSm - kBlockSmem) s.packs = 0;
-  // Blocks that share the columns: as many as an SM holds at 512 threads (or of
-  // the long columns' dG shares of at least 64 columns), each with the
-  // stages that their share of its memory allows
-  const int per_sm = std::max(1, 512 / s.threads);
+  // Blocks that share the columns: as many as an SM holds (or of the long columns'
+  // dG shares of at least 64 columns), each with the stages that its share of
+  // the memory allows, on the grid two at least
+  int per_sm = std::max(1, (g && s.packs <= 2 ? 1024 : 512) / s.threads);
+  while (g && per_sm > 1 && kSmemPerSm / per_sm - kBlockSmem < 2 * stage_bytes) --per_sm;
+  while (per_sm > 1 && kSmemPerSm / per_sm - kBlockSmem < stage_bytes) --per_sm;
   const int stages = (int)std::min<long long>(
       kMostStages, std::max<long long>(1, (kSmemPerSm / per_sm - kBlockSmem) / stage_bytes));
   const size_t smem = (size_t)(stages * stage_bytes);
@@ -872,7 +887,7 @@ int rmsgrad_entry(int m, int n, const T* dY, int lddy, const T* H, int ldh, cons
     if (dG != nullptr) {
       const int share = (n + blocks - 1) / blocks;
       e = launch_after(rmsgrad_weight_kernel<T>, dim3((m + 32 * kPack - 1) / (32 * kPack), blocks),
-                       dim3(32, kTall), 0, st, a, share);
+                       dim3(32, kDeepRows), 0, st, a, share);
       ++kernels;
     }
     if (e == cudaSuccess)
