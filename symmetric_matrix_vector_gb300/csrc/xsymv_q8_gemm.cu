@@ -59,11 +59,6 @@ bool map_rows(CUtensorMap* map, CUtensorMapDataType type, int bytes, const void*
                 CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
-bool map_halves(CUtensorMap* map, const __half* base, long long width, long long rows,
-                int box_rows) {
-  return map_rows(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, base, width, rows, width * 2, box_rows);
-}
-
 Prepare prepare_of(const int8_t* q, long long ldq, int rows, int k, long long width, void* out,
                    bool halves) {
   Prepare c{q, ldq, rows, k, width, out, halves, k % 16 == 0 && on_grid(q, ldq), 8};
@@ -115,77 +110,96 @@ int* status_word(cudaStream_t st, int* status, int* epoch) {
   return static_cast<int*>(workspace(256, st, status, 0, epoch));
 }
 
-// lets the kernel have its shared memory, once for each device
-template <int CTAS, int BN, bool RAW>
-cudaError_t allow_smem() {
+// lets `kernel` have its shared memory, once for each device
+template <auto kernel>
+cudaError_t allow_smem(int smem) {
   static std::atomic<unsigned long long> done{0};
   const int d = current_device_index();
   const unsigned long long bit = d >= 0 ? 1ull << d : 0;
   if (bit != 0 && (done.load() & bit) != 0) return cudaSuccess;
-  const cudaError_t e = cudaFuncSetAttribute(
-      gemmq_stream<CTAS, BN, RAW>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-      Stream<CTAS, BN, RAW>::kSmem);
+  const cudaError_t e =
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e == cudaSuccess) done.fetch_or(bit);
   return e;
 }
 
-template <int CTAS, int BN, bool RAW>
-int gemmq_streamed(const GemmqArgs& a, int split, cudaStream_t st) {
-  using S = Stream<CTAS, BN, RAW>;
-  const int steps = (int)((a.k + (long long)kStepDepth - 1) / kStepDepth);
-  const long long kp = (long long)steps * kStepDepth, ldo = (a.k + 15LL) / 16 * 16;
-  // tensor copies need 16-byte boundaries: what is not on them is copied first
-  const bool move_w = !on_grid(a.W, a.ldw), move_x = RAW && !on_grid(a.X, a.ldx);
+// The operands of a tiled product as its tensor copies take them: W in 8 bits and X in
+// 8 bits or (`halves`) as halves of a depth that is a multiple of kStepDepth.
+// What is not on 16-byte boundaries is copied first, in one launch.
+struct Operands {
+  CUtensorMap w, x;
+  int *status, epoch, steps, kernels;
+};
+int prepare_operands(const GemmqArgs& a, bool halves, int rows_x, cudaStream_t st, Operands* o) {
+  o->steps = (int)((a.k + (long long)kStepDepth - 1) / kStepDepth);
+  const long long kp = (long long)o->steps * kStepDepth, ldo = (a.k + 15LL) / 16 * 16;
+  const bool move_w = !on_grid(a.W, a.ldw), move_x = halves || !on_grid(a.X, a.ldx);
   Pieces pieces;
   const size_t at_w = move_w ? pieces.add((size_t)a.m * ldo) : 0;
-  const size_t at_x = RAW ? (move_x ? pieces.add((size_t)a.n * ldo) : 0)
-                              : pieces.add((size_t)a.n * kp * 2);
-  int status = XSYMV_OK, epoch = 0, kernels = 1;
-  int* const word = status_word(st, &status, &epoch);
-  if (word == nullptr) return status;
+  const size_t at_x = move_x ? pieces.add((size_t)a.n * (halves ? kp * 2 : ldo)) : 0;
+  int status = XSYMV_OK;
+  o->epoch = 0, o->kernels = 1;
+  o->status = status_word(st, &status, &o->epoch);
+  if (o->status == nullptr) return status;
   char* ws = nullptr;
   if (pieces.bytes > 0) {
     ws = static_cast<char*>(workspace(pieces.bytes, st, &status, kSlotOperands, nullptr));
     if (ws == nullptr) return status;
   }
-  const int8_t* w = a.W;
-  const int8_t* x = a.X;
-  long long ldw = a.ldw, ldx = a.ldx;
   Prepare pw{}, px{};
   pw.along = px.along = 8;
-  if (move_w) {
-    pw = prepare_of(a.W, a.ldw, a.m, a.k, ldo, ws + at_w, false);
-    w = static_cast<int8_t*>(pw.out), ldw = ldo;
-  }
-  CUtensorMap map_w, map_x;
-  bool mapped;
-  if (RAW) {
-    if (move_x) {
-      px = prepare_of(a.X, a.ldx, a.n, a.k, ldo, ws + at_x, false);
-      x = static_cast<int8_t*>(px.out), ldx = ldo;
-    }
-    mapped = map_rows(&map_x, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, x, a.k, a.n, ldx, BN);
-  } else {
-    px = prepare_of(a.X, a.ldx, a.n, a.k, kp, ws + at_x, true);
-    mapped = map_halves(&map_x, static_cast<__half*>(px.out), kp, a.n, BN / CTAS);
-  }
-  mapped = mapped && map_rows(&map_w, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, w, a.k, a.m, ldw, 128);
-  if (!mapped) return XSYMV_ERR_CUDA;
-  cudaError_t e = cudaSuccess;
+  if (move_w) pw = prepare_of(a.W, a.ldw, a.m, a.k, ldo, ws + at_w, false);
+  if (move_x) px = prepare_of(a.X, a.ldx, a.n, a.k, halves ? kp : ldo, ws + at_x, halves);
+  const void* w = move_w ? pw.out : a.W;
+  const void* x = move_x ? px.out : a.X;
+  if (!map_rows(&o->w, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, w, a.k, a.m, move_w ? ldo : a.ldw, 128))
+    return XSYMV_ERR_CUDA;
+  if (halves ? !map_rows(&o->x, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, x, kp, a.n, kp * 2, rows_x)
+             : !map_rows(&o->x, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, x, a.k, a.n,
+                         move_x ? ldo : a.ldx, rows_x))
+    return XSYMV_ERR_CUDA;
   if (pw.rows + px.rows > 0) {
-    e = launch_prepare(pw, px, st);
-    ++kernels;
+    const cudaError_t e = launch_prepare(pw, px, st);
+    if (e != cudaSuccess) {
+      record_cuda_error(e);
+      return XSYMV_ERR_CUDA;
+    }
+    ++o->kernels;
   }
-  if (e == cudaSuccess) e = allow_smem<CTAS, BN, RAW>();
-  if (e == cudaSuccess) {
-    const long long tiles_m = (a.m + S::kChannels - 1LL) / S::kChannels;
-    const long long tiles_n = (a.n + BN - 1LL) / BN;
-    const int cluster = CTAS == 2 ? 2 : split;
-    e = launch_cluster(gemmq_stream<CTAS, BN, RAW>, (unsigned)(tiles_m * tiles_n * cluster), cluster,
-                       S::kThreads, S::kSmem, CTAS == 1, st, map_w, map_x, a, (int)tiles_n, steps, split, word,
-                       epoch, wait_limit_ns(), test_extra_tx());
-  }
-  return launched(e, kernels, st, word, epoch);
+  return XSYMV_OK;
+}
+
+template <int BN, bool RAW>
+int gemmq_streamed(const GemmqArgs& a, int split, cudaStream_t st) {
+  using S = Stream<BN, RAW>;
+  Operands o;
+  const int r = prepare_operands(a, !RAW, BN, st, &o);
+  if (r != XSYMV_OK) return r;
+  cudaError_t e = allow_smem<gemmq_stream<BN, RAW>>(S::kSmem);
+  const long long tiles_m = (a.m + 127LL) / 128, tiles_n = (a.n + BN - 1LL) / BN;
+  if (e == cudaSuccess)
+    e = launch_cluster(gemmq_stream<BN, RAW>, (unsigned)(tiles_m * tiles_n * split), split,
+                       S::kThreads, S::kSmem, true, st, o.w, o.x, a, (int)tiles_n, o.steps, split,
+                       o.status, o.epoch, wait_limit_ns(), test_extra_tx());
+  return launched(e, o.kernels, st, o.status, o.epoch);
+}
+
+template <int TOKENS>
+int gemmq_paired(const GemmqArgs& a, int sms, cudaStream_t st) {
+  using S = Pairs<TOKENS>;
+  Operands o;
+  const int r = prepare_operands(a, true, S::kTokens / 2, st, &o);
+  if (r != XSYMV_OK) return r;
+  cudaError_t e = allow_smem<gemmq_pairs<TOKENS>>(S::kSmem);
+  TileOrder order;
+  order.tiles_m = (int)((a.m + 255LL) / 256);
+  order.tiles_n = (int)((a.n + S::kTokens - 1LL) / S::kTokens);
+  order.tiles = order.tiles_m * order.tiles_n;
+  if (e == cudaSuccess)
+    e = launch_cluster(gemmq_pairs<TOKENS>, (unsigned)(2 * std::min(order.tiles, sms / 2)), 2, S::kThreads,
+                       S::kSmem, false, st, o.w, o.x, a, order, o.steps, o.status, o.epoch,
+                       wait_limit_ns(), test_extra_tx());
+  return launched(e, o.kernels, st, o.status, o.epoch);
 }
 
 // CTAs that share a tile's depth: twice as many while they all fit on the SMs
@@ -232,20 +246,23 @@ int gemmq_entry(char type, int m, int n, int k, float alpha, const int8_t* W, in
   const long long rows = (m + 127LL) / 128;   // tiles of 128 channels
   if (n <= 64) {
     const int split = depth_split(rows, steps, 2LL * sms);
-    if (n <= 32) return gemmq_streamed<1, 32, true>(a, split, st);
+    if (n <= 32) return gemmq_streamed<32, true>(a, split, st);
     // X's halves made in the tile's CTAs or once beforehand (64 tokens; 4096 x 4096: 11.5
     // against 13.1 us, 32768 x 8192: 63 against 53)
-    if ((long long)m * k <= 1LL << 26) return gemmq_streamed<1, 64, true>(a, split, st);
-    return gemmq_streamed<1, 64, false>(a, split, st);
+    if ((long long)m * k <= 1LL << 26) return gemmq_streamed<64, true>(a, split, st);
+    return gemmq_streamed<64, false>(a, split, st);
   }
-  // 128 x 128 on one SM or 256 x 256 on two, whichever ends first by the clocks that
-  // a step takes (measured: 800 and 1180)
-  const long long small = rows * ((n + 127LL) / 128), large = (rows + 1) / 2 * ((n + 255LL) / 256);
+  // 128 x 128 a CTA, or 256 x 192 or 256 x 256 a pair, whichever ends first by the clocks
+  // that a step, a tile and a call take (measured)
+  const auto up = [](long long x, long long by) { return (x + by - 1) / by; };
+  const long long small = rows * up(n, 128), pairs = sms / 2;
   const int split = depth_split(small, steps, sms);
-  const long long clocks_small = (small * split + sms - 1) / sms * ((steps + split - 1) / split) * 800;
-  const long long clocks_large = (large * 2 + sms - 1) / sms * steps * 1180LL;
-  if (clocks_small <= clocks_large) return gemmq_streamed<1, 128, false>(a, split, st);
-  return gemmq_streamed<2, 256, false>(a, 1, st);
+  const long long clocks_128 = up(small * split, sms) * (up(steps, split) * 800 + 8000);
+  const long long clocks_192 = up(up(rows, 2) * up(n, 192), pairs) * steps * 780 + 12000;
+  const long long clocks_256 = up(up(rows, 2) * up(n, 256), pairs) * (steps * 1040LL + 9000);
+  if (clocks_128 <= std::min(clocks_192, clocks_256)) return gemmq_streamed<128, false>(a, split, st);
+  if (clocks_192 <= clocks_256) return gemmq_paired<192>(a, sms, st);
+  return gemmq_paired<256>(a, sms, st);
 }
 
 }  // namespace

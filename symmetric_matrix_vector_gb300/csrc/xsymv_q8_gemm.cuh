@@ -277,10 +277,10 @@ __global__ void __launch_bounds__(256) prepare_kernel(Prepare a, Prepare b, int 
 // halves of it on the way to tensor memory, and the tensor cores take their
 // first operand from there.  (In shared memory the halves would cost four
 // times their 8-bit bytes of its bandwidth, more than an SM has at the rate W
-// streams in.)  One tile a CTA, or 256 x 256 a pair; small shapes fit twice on an
-// SM, so that one's ends overlap the other's middle.  `split` CTAs of a cluster
-// share a tile's depth when there are few tiles and add their accumulators
-// through each other's shared memory, in rank order.
+// streams in.)  gemmq_stream: one tile a CTA; narrow ones fit twice on an SM, so that
+// one's ends overlap the other's middle.  `split` CTAs of a cluster share a tile's depth
+// when there are few tiles and add their accumulators through each other's shared
+// memory, in rank order.  gemmq_pairs, below: large products.
 //
 // RAW: X too arrives as 8-bit integers and four more warps make its halves in shared
 // memory, so the call is one kernel.  Else X's halves come from prepare_kernel.
@@ -288,11 +288,11 @@ __global__ void __launch_bounds__(256) prepare_kernel(Prepare a, Prepare b, int 
 // Warp 0 copies W, warp 1 copies X, warp 2 multiplies, warp 3 holds the tensor memory,
 // warps 4 to 11 convert W and store the results, warps 12 to 15 (RAW) convert X.
 constexpr int kStepDepth = 128;   // of a step: 128 bytes of W, 256 of X's halves
-template <int CTAS, int BN, bool RAW>
+constexpr int kStepBytesW = 128 * kStepDepth;
+template <int BN, bool RAW>
 struct Stream {
   static constexpr bool kTwice = BN <= 64;   // two CTAs an SM
-  static constexpr int kChannels = 128 * CTAS;
-  static constexpr int kBytesW = 128 * kStepDepth, kHalfX = BN / CTAS * 128;
+  static constexpr int kBytesW = kStepBytesW, kHalfX = BN * 128;
   static constexpr int kBytesX = 2 * kHalfX, kBytesRaw = RAW ? BN * kStepDepth : 0;
   // steps of W, of X's halves and of W's halves in tensor memory, of raw X
   static constexpr int kStagesA = kTwice ? 2 : 4, kStagesX = kStagesA, kStagesRaw = RAW ? 2 : 0;
@@ -376,7 +376,7 @@ __device__ __forceinline__ void store_result(const GemmqArgs& a, const TileResul
 #pragma unroll
     for (int e = 0; e < 4; ++e, y += a.ldy) {
       if (t.j + c + e >= a.n || i >= a.m) break;
-      T r[P];
+      alignas(4) T r[P];
 #pragma unroll
       for (int q = 0; q < P; ++q) {
         float x = v[q][e] * t.token[c + e];
@@ -391,14 +391,58 @@ __device__ __forceinline__ void store_result(const GemmqArgs& a, const TileResul
   }
 }
 
-template <int CTAS, int BN, bool RAW>
-__global__ void __launch_bounds__(Stream<CTAS, BN, RAW>::kThreads,
-                                  Stream<CTAS, BN, RAW>::kTwice ? 2 : 1)
+// One step of W from shared memory to halves in tensor memory: this thread's channel
+// (`row` of the stage) and its group's half of the depth.  False, for the whole warp,
+// if a wait ran out.
+__device__ __forceinline__ bool convert_step(uint32_t stage, int row, int group, uint32_t full,
+                                             uint32_t full_parity, uint32_t empty,
+                                             uint32_t empty_parity, uint32_t to,
+                                             volatile int* dead, unsigned long long limit_ns) {
+  bool ok = wait_or_dead(full, full_parity, dead, limit_ns);
+  if (!__all_sync(0xffffffffu, ok)) return false;
+  uint4 q[4];
+#pragma unroll
+  for (int c = 0; c < 4; ++c)
+    q[c] = lds128(stage + row * 128 + (((4 * group + c) ^ (row & 7)) << 4));
+  ok = wait_or_dead(empty, empty_parity, dead, limit_ns);
+  if (!__all_sync(0xffffffffu, ok)) return false;
+  tensor_fence_after();
+#pragma unroll
+  for (int c = 0; c < 4; c += 2) {
+    uint32_t h[16];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      halves_of(q[c + e].x, h[8 * e], h[8 * e + 1]);
+      halves_of(q[c + e].y, h[8 * e + 2], h[8 * e + 3]);
+      halves_of(q[c + e].z, h[8 * e + 4], h[8 * e + 5]);
+      halves_of(q[c + e].w, h[8 * e + 6], h[8 * e + 7]);
+    }
+    tmem_store16(to + group * 32 + 8 * c, h);
+  }
+  tmem_stored();
+  tensor_fence_before();
+  __syncwarp();
+  return true;
+}
+// The products of one step: W's halves at `w` in tensor memory, X's in shared memory as
+// two tiles of 64 halves a row, `half_x` bytes each; issued by a whole warp
+template <int CTAS>
+__device__ __forceinline__ void multiply_step(uint32_t acc, uint32_t w, uint32_t x, int half_x,
+                                              uint32_t idesc, bool first, uint32_t one) {
+  const uint64_t lo = tile_descriptor(x), hi = tile_descriptor(x + half_x);
+#pragma unroll
+  for (int q = 0; q < kStepDepth / 16; ++q)   // 16 halves: 8 columns, 2 units of the descriptor
+    mma_half_tmem<CTAS>(acc, w + 8 * q, (q < 4 ? lo : hi) + 2 * (q % 4), idesc, !first || q > 0,
+                        one);
+}
+
+template <int BN, bool RAW>
+__global__ void __launch_bounds__(Stream<BN, RAW>::kThreads, Stream<BN, RAW>::kTwice ? 2 : 1)
     gemmq_stream(const __grid_constant__ CUtensorMap map_w,
                  const __grid_constant__ CUtensorMap map_x, GemmqArgs a, int tiles_n, int steps,
                  int split, int* status, int epoch, unsigned long long limit_ns,
                  uint32_t extra_tx) {
-  using S = Stream<CTAS, BN, RAW>;
+  using S = Stream<BN, RAW>;
   // the ring that X's copies fill: raw X, or its halves
   constexpr int COPIES = RAW ? S::kStagesRaw : S::kStagesX;
   extern __shared__ uint8_t raw_smem[];
@@ -413,18 +457,15 @@ __global__ void __launch_bounds__(Stream<CTAS, BN, RAW>::kThreads,
   const uint32_t a_full = x_empty + 8 * COPIES, a_empty = a_full + 8 * S::kStagesA;
   const uint32_t acc_full = a_empty + 8 * S::kStagesA;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int cluster = CTAS == 2 ? 2 : split;
-  const int rank = cluster > 1 ? (int)cluster_rank() : 0;
+  const int rank = split > 1 ? (int)cluster_rank() : 0;
   // tiles that share W side by side: it is read from HBM once
-  const int tile = blockIdx.x / cluster, tm = tile / tiles_n, tn = tile - tm * tiles_n;
+  const int tile = blockIdx.x / split, tm = tile / tiles_n, tn = tile - tm * tiles_n;
   // this CTA's channels and tokens, and its steps of the depth
-  const int row_w = tm * S::kChannels + (CTAS == 2 ? rank * 128 : 0);
-  const int row_x = tn * BN + (CTAS == 2 ? rank * (BN / CTAS) : 0);
-  const int part = CTAS == 2 ? 0 : rank;
-  const int s0 = (int)((long long)steps * part / split);
-  const int mine = (int)((long long)steps * (part + 1) / split) - s0;
+  const int row_w = tm * 128, row_x = tn * BN;
+  const int s0 = (int)((long long)steps * rank / split);
+  const int mine = (int)((long long)steps * (rank + 1) / split) - s0;
 
-  if (CTAS == 1) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (threadIdx.x == 0) {
     // the first steps of W on their way to L2 while the predecessor still runs
     for (int u = 0; u < min(mine, 8); ++u)
@@ -438,17 +479,16 @@ __global__ void __launch_bounds__(Stream<CTAS, BN, RAW>::kThreads,
       mbar_init(x_empty + 8 * s, RAW ? 4 : 1);
     }
     for (int s = 0; s < S::kStagesA; ++s) {
-      mbar_init(a_full + 8 * s, (RAW ? 12 : 8) * CTAS);
+      mbar_init(a_full + 8 * s, RAW ? 12 : 8);
       mbar_init(a_empty + 8 * s, 1);
     }
     mbar_init(acc_full, 1);
     dead_word = 0;
     mbar_init_fence();
   }
-  if (warp == 3) tmem_alloc<CTAS>(smem_addr(&tmem_word), S::kColumns);
+  if (warp == 3) tmem_alloc<1>(smem_addr(&tmem_word), S::kColumns);
   tensor_fence_before();
   __syncthreads();
-  if (CTAS == 2) cluster_sync();
   tensor_fence_after();
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const uint32_t tmem = tmem_word, tmem_a = tmem + BN;
@@ -461,7 +501,6 @@ __global__ void __launch_bounds__(Stream<CTAS, BN, RAW>::kThreads,
     const bool w = warp == 0;
     const int stages = w ? S::kStagesW : COPIES;
     const uint32_t full = w ? w_full : x_full, empty = w ? w_empty : x_empty;
-    const uint32_t lead_full = CTAS == 2 && !w ? cluster_address(x_full, 0) : full;
     int u = 0;
     for (; u < mine; ++u) {
       const int stage = u % stages, depth = (s0 + u) * kStepDepth;
@@ -474,10 +513,10 @@ __global__ void __launch_bounds__(Stream<CTAS, BN, RAW>::kThreads,
         mbar_arrive_expect_tx(bar, S::kBytesRaw + extra_tx);
         tensor_g2s<1>(ring + S::kAtRaw + stage * S::kBytesRaw, &map_x, depth, row_x, bar);
       } else {
-        if (CTAS == 1 || rank == 0) mbar_arrive_expect_tx(bar, CTAS * S::kBytesX + extra_tx);
-        const uint32_t lead = lead_full + 8 * stage, at = ring + S::kAtX + stage * S::kBytesX;
-        tensor_g2s<CTAS>(at, &map_x, depth, row_x, lead);
-        tensor_g2s<CTAS>(at + S::kHalfX, &map_x, depth + kDepth, row_x, lead);
+        mbar_arrive_expect_tx(bar, S::kBytesX + extra_tx);
+        const uint32_t at = ring + S::kAtX + stage * S::kBytesX;
+        tensor_g2s<1>(at, &map_x, depth, row_x, bar);
+        tensor_g2s<1>(at + S::kHalfX, &map_x, depth + kDepth, row_x, bar);
       }
     }
     // the arrivals of the last products reach this CTA before it may exit
@@ -496,9 +535,9 @@ __global__ void __launch_bounds__(Stream<CTAS, BN, RAW>::kThreads,
         }
       ok = false;
     }
-  } else if (warp == 2 && (CTAS == 1 || rank == 0)) {
+  } else if (warp == 2) {
     // ---- products
-    constexpr uint32_t idesc = half_mma(S::kChannels, BN);
+    constexpr uint32_t idesc = half_mma(128, BN);
     const uint32_t one = elect_one();
     for (int u = 0; u < mine; ++u) {
       const int sx = u % S::kStagesX, sa = u % S::kStagesA;
@@ -507,67 +546,30 @@ __global__ void __launch_bounds__(Stream<CTAS, BN, RAW>::kThreads,
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       tensor_fence_after();
-      const uint32_t at = ring + S::kAtX + sx * S::kBytesX;
-      const uint64_t lo = tile_descriptor(at), hi = tile_descriptor(at + S::kHalfX);
-      const uint32_t ta = tmem_a + sa * S::kColumnsA;
-#pragma unroll
-      for (int q = 0; q < kStepDepth / 16; ++q)
-        mma_half_tmem<CTAS>(tmem, ta + 8 * q, (q < 4 ? lo : hi) + 2 * (q % 4), idesc,
-                            u > 0 || q > 0, one);
-      if (!RAW) mma_commit<CTAS>(x_empty + 8 * sx, one);
-      mma_commit<CTAS>(a_empty + 8 * sa, one);
+      multiply_step<1>(tmem, tmem_a + sa * S::kColumnsA, ring + S::kAtX + sx * S::kBytesX,
+                       S::kHalfX, idesc, u == 0, one);
+      if (!RAW) mma_commit<1>(x_empty + 8 * sx, one);
+      mma_commit<1>(a_empty + 8 * sa, one);
     }
-    if (ok) mma_commit<CTAS>(acc_full, one);
+    if (ok) mma_commit<1>(acc_full, one);
   } else if (warp >= 4 && warp < 12) {
     // ---- W to halves: a thread a channel, a group of four warps each half of the depth.
     // Every warp takes every step: a parity wait that skipped a phase would match the
     // one before it.
-    const int row = quarter * 32 + lane;
-    const uint32_t lead_full = CTAS == 2 ? cluster_address(a_full, 0) : a_full;
+    const uint32_t to = tmem_a + ((uint32_t)(quarter * 32) << 16);
     for (int u = 0; u < mine; ++u) {
       const int stage = u % S::kStagesW, sa = u % S::kStagesA;
-      ok = wait_or_dead(w_full + 8 * stage, u / S::kStagesW & 1, dead, limit_ns);
-      if (!__all_sync(0xffffffffu, ok)) {
-        ok = false;
-        break;
-      }
-      const uint32_t at = ring + stage * S::kBytesW + row * 128;
-      uint4 q[4];
-#pragma unroll
-      for (int c = 0; c < 4; ++c) q[c] = lds128(at + (((4 * group + c) ^ (row & 7)) << 4));
-      ok = wait_or_dead(a_empty + 8 * sa, (u / S::kStagesA & 1) ^ 1, dead, limit_ns);
-      if (!__all_sync(0xffffffffu, ok)) {
-        ok = false;
-        break;
-      }
-      tensor_fence_after();
-      const uint32_t to =
-          tmem_a + ((uint32_t)(quarter * 32) << 16) + sa * S::kColumnsA + group * 32;
-#pragma unroll
-      for (int c = 0; c < 4; c += 2) {
-        uint32_t h[16];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          halves_of(q[c + e].x, h[8 * e], h[8 * e + 1]);
-          halves_of(q[c + e].y, h[8 * e + 2], h[8 * e + 3]);
-          halves_of(q[c + e].z, h[8 * e + 4], h[8 * e + 5]);
-          halves_of(q[c + e].w, h[8 * e + 6], h[8 * e + 7]);
-        }
-        tmem_store16(to + 8 * c, h);
-      }
-      tmem_stored();
-      tensor_fence_before();
-      __syncwarp();
+      ok = convert_step(ring + stage * S::kBytesW, quarter * 32 + lane, group, w_full + 8 * stage,
+                        u / S::kStagesW & 1, a_empty + 8 * sa, (u / S::kStagesA & 1) ^ 1,
+                        to + sa * S::kColumnsA, dead, limit_ns);
+      if (!ok) break;
       if (lane == 0) {
         // the stage goes back to the copies only now that its integers have reached
         // tensor memory: an arrival right after the loads, even behind a fence, can
         // overtake loads on their way (once in some 60 000 calls a row of W was that of
         // a later step)
         mbar_arrive(w_empty + 8 * stage);
-        if (CTAS == 2)
-          mbar_arrive_cluster(lead_full + 8 * sa);
-        else
-          mbar_arrive(a_full + 8 * sa);
+        mbar_arrive(a_full + 8 * sa);
       }
     }
     // the accumulators, complete
@@ -641,10 +643,7 @@ __global__ void __launch_bounds__(Stream<CTAS, BN, RAW>::kThreads,
         store_columns<__nv_bfloat16>(a, from, i, j0, group * 16, 32, BN, channel, token_scale);
     }
     tensor_fence_before();
-    if (CTAS == 2)
-      cluster_sync();
-    else
-      __syncthreads();
+    __syncthreads();
   } else {
     // the accumulators' columns q*width .. to CTA q of the cluster, into the shared memory
     // that every CTA has finished with
@@ -684,7 +683,214 @@ __global__ void __launch_bounds__(Stream<CTAS, BN, RAW>::kThreads,
   if (*dead != 0 && threadIdx.x == 0) atomicMax(status, epoch);
   __syncwarp();
   tensor_fence_after();
-  if (warp == 3) tmem_free<CTAS>(tmem, S::kColumns);
+  if (warp == 3) tmem_free<1>(tmem, S::kColumns);
+}
+
+// ---------------------------------------------------------- large products --
+
+// Tiles of 256 channels by TOKENS tokens, each formed by a pair of CTAs (either holds 128
+// channels and half of the tokens' operands).  A pair takes one tile after the other.
+// 192 tokens: two sets of accumulators (2 * 192 of tensor memory's 512 columns, the rest
+// two steps of W's halves), so that eight warps store a tile while the next is formed
+// (8192 x 2048 x 2048: 49 us; one set of 256: 67).  256 tokens, one set: where a tile a pair
+// does it all (8192 x 8192 x 512: 49 us against 65).  Not launched while its predecessor
+// runs, nor its successor while it does.
+//
+// Warps 0 and 1 copy W and X, warp 2 multiplies (the first CTA's), warp 3 holds the
+// tensor memory, 4 to 11 convert W, 12 to 19 store.
+template <int TOKENS>
+struct Pairs {
+  static constexpr int kTokens = TOKENS, kHalfX = kTokens / 2 * 128, kBytesX = 2 * kHalfX;
+  static constexpr int kSets = TOKENS <= 192 ? 2 : 1;
+  static constexpr int kStages = 4, kStagesA = 4 / kSets, kColumnsA = kStepDepth / 2;
+  static constexpr int kThreads = 640;
+  static constexpr int kAtX = kStages * kStepBytesW;
+  static constexpr int kSmem = kAtX + kStages * kBytesX + 1024;
+  static_assert(kSets * kTokens + kStagesA * kColumnsA <= 512, "tensor memory");
+};
+struct TileOrder {
+  int tiles_m, tiles_n, tiles;
+  // Tiles that run at the same time are near one another in both directions:
+  // bands of 8 tiles of tokens, channels advancing within a band
+  __device__ __forceinline__ void at(int t, int& tm, int& tn) const {
+    const int band = 8 * tiles_m, b = t / band, in = t - b * band;
+    const int width = min(8, tiles_n - 8 * b);
+    tm = in / width;
+    tn = 8 * b + in - tm * width;
+  }
+};
+
+template <int TOKENS>
+__global__ void __launch_bounds__(Pairs<TOKENS>::kThreads, 1)
+    gemmq_pairs(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
+                GemmqArgs a, TileOrder order, int steps, int* status, int epoch,
+                unsigned long long limit_ns, uint32_t extra_tx) {
+  using S = Pairs<TOKENS>;
+  extern __shared__ uint8_t raw_smem[];
+  __shared__ alignas(8) uint64_t bar_words[4 * S::kStages + 2 * S::kStagesA + 2 * S::kSets];
+  __shared__ uint32_t tmem_word;
+  __shared__ int dead_word;
+  __shared__ float token_scale[S::kSets][S::kTokens];
+  volatile int* const dead = &dead_word;
+  const uint32_t ring = (smem_addr(raw_smem) + 1023u) & ~1023u;
+  const uint32_t w_full = smem_addr(bar_words), w_empty = w_full + 8 * S::kStages;
+  const uint32_t x_full = w_empty + 8 * S::kStages, x_empty = x_full + 8 * S::kStages;
+  const uint32_t a_full = x_empty + 8 * S::kStages, a_empty = a_full + 8 * S::kStagesA;
+  const uint32_t acc_full = a_empty + 8 * S::kStagesA, acc_empty = acc_full + 8 * S::kSets;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const uint32_t rank = cluster_rank();
+  const int first_tile = blockIdx.x / 2, stride = gridDim.x / 2;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S::kStages; ++s) {
+      mbar_init(w_full + 8 * s, 1);
+      mbar_init(w_empty + 8 * s, 8);
+      mbar_init(x_full + 8 * s, 1);
+      mbar_init(x_empty + 8 * s, 1);
+    }
+    for (int s = 0; s < S::kStagesA; ++s) {
+      mbar_init(a_full + 8 * s, 16);
+      mbar_init(a_empty + 8 * s, 1);
+    }
+    for (int s = 0; s < S::kSets; ++s) {
+      mbar_init(acc_full + 8 * s, 1);
+      mbar_init(acc_empty + 8 * s, 16);
+    }
+    dead_word = 0;
+    mbar_init_fence();
+  }
+  if (warp == 3) tmem_alloc<2>(smem_addr(&tmem_word), 512);
+  tensor_fence_before();
+  __syncthreads();
+  cluster_sync();
+  tensor_fence_after();
+  const uint32_t tmem = tmem_word, tmem_a = tmem + S::kSets * S::kTokens;
+  const int group = (warp - 4) / 4 & 1, quarter = warp % 4;   // of warps 4 to 19
+  const uint32_t lane0 = (uint32_t)(quarter * 32) << 16;      // this warp's lanes of tensor memory
+  bool ok = true;
+
+  if (warp < 2 && lane == 0) {
+    // ---- copies of W (warp 0) or X (warp 1)
+    const bool w = warp == 0;
+    const uint32_t full = w ? w_full : x_full, empty = w ? w_empty : x_empty;
+    const uint32_t lead_x = cluster_address(x_full, 0);
+    unsigned u = 0;
+    for (int t = first_tile; ok && t < order.tiles; t += stride) {
+      int tm, tn;
+      order.at(t, tm, tn);
+      const int row_w = tm * 256 + (int)rank * 128;
+      const int row_x = tn * S::kTokens + (int)rank * (S::kTokens / 2);
+      for (int s = 0; s < steps; ++s, ++u) {
+        const int stage = u % S::kStages, depth = s * kStepDepth;
+        ok = wait_or_dead(empty + 8 * stage, (u / S::kStages & 1) ^ 1, dead, limit_ns);
+        if (!ok) break;
+        if (w) {
+          mbar_arrive_expect_tx(full + 8 * stage, kStepBytesW + extra_tx);
+          tensor_g2s<1>(ring + stage * kStepBytesW, &map_w, depth, row_w, full + 8 * stage);
+        } else {
+          if (rank == 0) mbar_arrive_expect_tx(full + 8 * stage, 2 * S::kBytesX + extra_tx);
+          const uint32_t at = ring + S::kAtX + stage * S::kBytesX, lead = lead_x + 8 * stage;
+          tensor_g2s<2>(at, &map_x, depth, row_x, lead);
+          tensor_g2s<2>(at + S::kHalfX, &map_x, depth + kDepth, row_x, lead);
+        }
+      }
+    }
+    const unsigned back = min(u, (unsigned)S::kStages);
+    if (ok) {
+      // what was copied has been read, and the arrivals of the last products have reached
+      // this CTA, before it may exit
+      for (unsigned s = u - back; ok && s != u; ++s)
+        ok = wait_or_dead(empty + 8 * (s % S::kStages), s / S::kStages & 1, dead, limit_ns);
+      for (unsigned s = u - min(u, (unsigned)S::kStagesA); ok && !w && s != u; ++s)
+        ok = wait_or_dead(a_empty + 8 * (s % S::kStagesA), s / S::kStagesA & 1, dead, limit_ns);
+    } else {
+      // given up: copies in flight land, or have had their time to
+      const unsigned long long t0 = global_ns();
+      for (unsigned s = u - back; s != u; ++s)
+        while (!mbar_try_wait(full + 8 * (s % S::kStages), s / S::kStages & 1) &&
+               global_ns() - t0 <= limit_ns) {
+        }
+    }
+  } else if (warp == 2 && rank == 0) {
+    // ---- products
+    constexpr uint32_t idesc = half_mma(256, S::kTokens);
+    const uint32_t one = elect_one();
+    unsigned u = 0, n = 0;   // steps, tiles so far
+    for (int t = first_tile; ok && t < order.tiles; t += stride, ++n) {
+      const int set = n % S::kSets;
+      ok = wait_or_dead(acc_empty + 8 * set, (n / S::kSets & 1) ^ 1, dead, limit_ns);
+      ok = __all_sync(0xffffffffu, ok);
+      for (int s = 0; ok && s < steps; ++s, ++u) {
+        const int sx = u % S::kStages, sa = u % S::kStagesA;
+        ok = wait_or_dead(x_full + 8 * sx, u / S::kStages & 1, dead, limit_ns) &&
+             wait_or_dead(a_full + 8 * sa, u / S::kStagesA & 1, dead, limit_ns);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tensor_fence_after();
+        multiply_step<2>(tmem + set * S::kTokens, tmem_a + sa * S::kColumnsA,
+                         ring + S::kAtX + sx * S::kBytesX, S::kHalfX, idesc, s == 0, one);
+        mma_commit<2>(x_empty + 8 * sx, one);
+        mma_commit<2>(a_empty + 8 * sa, one);
+      }
+      if (ok) mma_commit<2>(acc_full + 8 * set, one);
+    }
+  } else if (warp >= 4 && warp < 12) {
+    // ---- W to halves, step after step over all tiles
+    const uint32_t lead_full = cluster_address(a_full, 0);
+    unsigned u = 0;
+    for (int t = first_tile; ok && t < order.tiles; t += stride)
+      for (int s = 0; s < steps; ++s, ++u) {
+        const int stage = u % S::kStages, sa = u % S::kStagesA;
+        ok = convert_step(ring + stage * kStepBytesW, quarter * 32 + lane, group,
+                          w_full + 8 * stage, u / S::kStages & 1, a_empty + 8 * sa,
+                          (u / S::kStagesA & 1) ^ 1, tmem_a + lane0 + sa * S::kColumnsA, dead,
+                          limit_ns);
+        if (!ok) break;
+        if (lane == 0) {
+          mbar_arrive(w_empty + 8 * stage);
+          mbar_arrive_cluster(lead_full + 8 * sa);
+        }
+      }
+  } else if (warp >= 12) {
+    // ---- results: two warps for every 32 lanes, 16 tokens in turn
+    const uint32_t lead_empty = cluster_address(acc_empty, 0);
+    unsigned n = 0;
+    for (int t = first_tile; t < order.tiles; t += stride, ++n) {
+      const int set = n % S::kSets;
+      int tm, tn;
+      order.at(t, tm, tn);
+      const long long i = (long long)tm * 256 + (int)rank * 128 + quarter * 32 + lane;
+      const long long j = (long long)tn * S::kTokens;
+      const int c = (int)threadIdx.x - 384;
+      if (S::kSets == 1) asm volatile("bar.sync 1, 256;" ::: "memory");   // read by all
+      if (c < S::kTokens) token_scale[set][c] = j + c < a.n ? token_factor(a, j + c) : 0.f;
+      float channel = i < a.m && a.sw != nullptr ? a.sw[i] : 1.f;
+      if (ok) ok = wait_or_dead(acc_full + 8 * set, n / S::kSets & 1, dead, limit_ns);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) channel = __uint_as_float(0x7fc00000u);
+      asm volatile("bar.sync 1, 256;" ::: "memory");   // token_scale is complete
+      tensor_fence_after();
+      const uint32_t from = tmem + lane0 + set * S::kTokens;
+      if (a.type == 's')
+        store_columns<float>(a, from, i, j, group * 16, 32, S::kTokens, channel, token_scale[set]);
+      else if (a.type == 'h')
+        store_columns<__half>(a, from, i, j, group * 16, 32, S::kTokens, channel,
+                              token_scale[set]);
+      else
+        store_columns<__nv_bfloat16>(a, from, i, j, group * 16, 32, S::kTokens, channel,
+                                     token_scale[set]);
+      tensor_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(lead_empty + 8 * set);
+    }
+  }
+  __syncwarp();
+  if (!ok && lane == 0) atomicMax(status, epoch);
+  tensor_fence_before();
+  __syncthreads();
+  cluster_sync();
+  tensor_fence_after();
+  if (warp == 3) tmem_free<2>(tmem, 512);
 }
 
 }  // namespace xsymv

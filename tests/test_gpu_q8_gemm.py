@@ -58,6 +58,16 @@ def test_token_counts(n):
             check(kind, m, n, k, g, pad, off)
 
 
+@pytest.mark.parametrize("kind,m,n,k,pad,off", [
+    ("b", 8192, 2048, 256, 0, 0), ("h", 4099, 3001, 333, 1, 3), ("s", 2560, 6000, 128, 16, 0),
+    ("b", 300, 9000, 1, 0, 0), ("h", 10000, 1000, 200, 0, 1), ("s", 5000, 1537, 1000, 8, 0)])
+def test_many_tiles(kind, m, n, k, pad, off):
+    """more tiles than the GPU forms at once, odd edges, queued one behind another"""
+    g = gen(m + n)
+    for alpha, beta in ((1.0, 0.0), (0.5, -2.0), (1.0, 0.0)):
+        check(kind, m, n, k, g, pad, off, alpha, beta)
+
+
 @pytest.mark.parametrize("k", [1, 2, 15, 16, 31, 32, 33, 63, 64, 65, 100, 127, 128, 130, 255, 256,
                                1000, 1543, 4096, 5000, 16384])
 def test_depths(k):
@@ -158,7 +168,7 @@ def test_repeats_bitwise_on_another_stream(n):
     assert all(torch.equal(outs[0], y) for y in outs[1:])
 
 
-@pytest.mark.parametrize("n", [1, 3, 8, 13, 30, 37, 64, 100, 200, 500, 1500])
+@pytest.mark.parametrize("n", [1, 3, 8, 13, 30, 37, 64, 100, 200, 500, 1500, 4000])
 def test_many_calls_in_a_row(n):
     """calls queued behind one another, different operands in turn, give what each
     gives alone"""
@@ -287,7 +297,7 @@ def test_queued_weights(n):
 
 
 @pytest.mark.parametrize("m,n,k", [(700, 20, 640), (700, 64, 640), (700, 100, 640), (130, 50, 64),
-                                   (2048, 2048, 256)])
+                                   (2048, 2048, 256), (4096, 4096, 512)])
 def test_waits_that_run_out(m, n, k):
     """copies whose barrier expects bytes that never arrive (nothing faults): the
     kernel returns after the limit, Y is NaN, the status says so, and the next
