@@ -439,8 +439,9 @@ XSYMV_API int xgemv_selected_variant(char type);
 typedef struct { unsigned short bits; } xsymv_f16;    /* IEEE half     */
 typedef struct { unsigned short bits; } xsymv_bf16;   /* bfloat16      */
 
-/* scale[j] = max_i |X(i,j)| / 127,  Q(i,j) = X(i,j) / scale[j] rounded to the
- * nearest integer, ties to even (-127 .. 127).  A column of zeros (or one
+/* scale[j] = max_i |X(i,j)| / 127,  Q(i,j) = 127 X(i,j) / max_i |X(i,j)| rounded
+ * to the nearest integer, ties to even (-127 .. 127; of 16-bit types exactly, of
+ * float within 2^-22 of a tie either way).  A column of zeros (or one
  * so small that its scale rounds to zero) has scale 0 and Q 0.  A column
  * that holds an infinity or a NaN has scale NaN and Q 0, so that everything
  * computed from it is NaN.

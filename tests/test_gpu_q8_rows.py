@@ -60,6 +60,31 @@ def test_quant_and_dequant(kind, m, n):
             assert v.outside_untouched()
 
 
+@pytest.mark.parametrize("kind", ["h", "b"])
+def test_quant_rounds_16_bit_values_exactly(kind):
+    """127 x / max|x| to the nearest integer, ties to even, in whole numbers: values on
+    few bits, where ties are common, and every largest value a half or bfloat16 has"""
+    m, n = 600, 256
+    g = gen(77)
+    x = torch.randint(-255, 256, (n, m), generator=g, device="cuda").to(DTYPES[kind])
+    x[:, 0] = torch.arange(n, device="cuda").to(DTYPES[kind])      # some columns' largest
+    x[::2] = (x[::2] % 32).to(DTYPES[kind])
+    scale = torch.tensor([1.0, 2.0 ** -14, 2.0 ** 7], device="cuda")[torch.arange(n, device="cuda") % 3]
+    x = (x.float() * scale[:, None]).to(DTYPES[kind])
+    q = torch.empty((n, m), dtype=torch.int8, device="cuda")
+    s = torch.empty((n,), device="cuda")
+    assert xs.quant(kind, m, n, x, m, q, m, s) == 0
+    torch.cuda.synchronize()
+    num = torch.round(x.double() / scale.double()[:, None] * 256).long() * 127     # whole
+    top = torch.round(x.double().abs().amax(1) / scale.double() * 256).long()[:, None]
+    safe = torch.where(top > 0, top, torch.ones_like(top))
+    low = torch.div(num, safe, rounding_mode="floor")
+    twice = 2 * (num - low * safe)                                 # against one top
+    up = (twice > safe) | ((twice == safe) & (low % 2 != 0))
+    want = torch.where(top > 0, low + up.long(), torch.zeros_like(low))
+    assert torch.equal(q.long(), want)
+
+
 @pytest.mark.parametrize("kind", ["s", "h", "b"])
 def test_quant_special_columns(kind):
     """zeros, one value, an infinity, a NaN in any place, the type's largest and
