@@ -421,19 +421,24 @@ XSYMV_API int xgemv_selected_variant(char type);
  * All pointers are DEVICE pointers aligned to their element, owned by the
  * caller; any alignment beyond that and any leading dimension work (rows of
  * 16-byte aligned columns are faster).  Only the m elements of each column
- * are read or written, never the padding between columns.  Arrays written
+ * are used or written, never the padding between columns; a load takes whole
+ * aligned 16-byte pieces where at least one element of the column lies in them.
+ * Sizes go up to 2147418112 (2^31 - 2^16).  Arrays written
  * must not overlap other arguments, except where "in place" is said: then
  * pointer and leading dimension must both be the same.  m = 0 or n = 0
  * returns at once (x<rmsgrad> with n = 0 sets dG to 0 first).
  *
  * Work is enqueued on the library's stream and runs asynchronously, like
- * the SYMV calls; x<rmsgrad> and x<gemmq> keep partial results in library
- * workspaces per (device, stream), grown on demand.  Results are
- * bit-identical from run to run.  Every sum, norm and scale is formed in 32
+ * the SYMV calls; x<rmsgrad> (partial sums of dG) and x<gemmq> (operands as
+ * the tensor cores take them, when there are more than 8 tokens) use library
+ * workspaces per (device, stream), grown on demand.  A call may be captured into
+ * a graph once a call of its sizes has run on that stream (capture cannot
+ * allocate); the graph holds as long as no later call on the stream needs a
+ * larger workspace.  Results are bit-identical from run to run.  Every sum, norm and scale is formed in 32
  * bits or more, and a result is rounded to T once.
  *
  * Status: 0; the position of the first bad argument in its signature (a
- * negative size, a leading dimension below max(1, rows), eps negative or
+ * size out of range, a leading dimension below max(1, rows), eps negative or
  * NaN), with nothing enqueued; XSYMV_ERR_VALUE for a NULL pointer that is not
  * optional; or XSYMV_ERR_*. */
 typedef struct { unsigned short bits; } xsymv_f16;    /* IEEE half     */
@@ -473,7 +478,8 @@ XSYMV_API int xdequant_b(int m, int n, const signed char *Q, int ldq, const floa
  * H     NULL: not stored (ldh is not used).  In place: H may be X or R.
  * rstd  NULL: not stored.
  * Squares that overflow or underflow float are summed scaled: any finite H
- * has the norm of its definition.
+ * has the norm of its definition.  A column whose rstd is beyond float (eps = 0
+ * and H zero or next to it) has scale NaN and Q 0, as one that is not finite.
  * Bad arguments: 1 m, 2 n, 4 ldx, 6 ldr, 8 eps, 10 ldh, 12 ldq. */
 XSYMV_API int xrmsquant_s(int m, int n, const float *X, int ldx, const float *R, int ldr,
                           const float *G, float eps, float *H, int ldh, signed char *Q, int ldq,
@@ -513,8 +519,11 @@ XSYMV_API int xrmsgrad_b(int m, int n, const xsymv_bf16 *dY, int lddy, const xsy
  * sw, sx  NULL: all ones.
  * beta = 0: Y is written without being read.  alpha = 0 or k = 0: W, X and
  * the scales are not read; if then beta = 1, nothing is touched.
- * The sum of integer products is exact up to 2^24 in size (always, for
- * k <= 1040) and accumulated in float or int32 beyond.
+ * Products are exact and summed in float: the sum is exact while partial sums
+ * stay below 2^24 in size (always, for k <= 1024).
+ * The kernels for more than 8 tokens wait, with a limit, for their own copies;
+ * should one run out, Y's tile is NaN and xsymv_sync_status reports
+ * XSYMV_ERR_TIMEOUT.
  * Bad arguments: 1 m, 2 n, 3 k, 6 ldw, 9 ldx, 13 ldy. */
 XSYMV_API int xgemmq_s(int m, int n, int k, float alpha, const signed char *W, int ldw,
                        const float *sw, const signed char *X, int ldx, const float *sx,

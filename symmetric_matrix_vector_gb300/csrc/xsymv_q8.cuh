@@ -1,5 +1,5 @@
 // What the 8-bit linear-layer kernels share: the storage types, the rules of
-// the 8-bit rounding, and block-wide reductions in a fixed order.
+// the 8-bit rounding, packs of a column's elements at any alignment, launches.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -63,7 +63,9 @@ __device__ __forceinline__ Rounding rounding_of(float a) {
   r.inv = r.scale > 0.f ? 127.f / (a * r.pre) : 0.f;
   return r;
 }
+
 constexpr int kPack = 8;
+
 // ------------------------------------------------------ a column's elements --
 
 // a pack as 32-bit words, and as four pairs of floats
@@ -169,7 +171,7 @@ __device__ __forceinline__ void shift_words(uint32_t (&w)[M], unsigned off) {
 // GRID: every operand's columns start on the grid of 16-byte pieces (8-byte
 // ones of 8-bit elements) and are whole packs long, the usual case: a pack
 // is all of the column or all outside, and no element is looked at singly
-// (rmsquant 1024 x 16384 halves: 23 us without, 14 us with it).
+// (rmsquant of bfloat16, 128 x 16384: 26 us without, 7.0 with it; 1024 x 16384: 23.1, 21.2).
 template <bool GRID, class T>
 __device__ __forceinline__ Raw<T> load8(const T* row, int first, int m) {
   constexpr int N = Raw<T>::N, P = kPiece<T> / 4;
@@ -285,6 +287,10 @@ inline int launched(cudaError_t e, int kernels, cudaStream_t st, const int* stat
   return XSYMV_OK;
 }
 
+// sizes that are refused: negative ones, and ones so large that an index rounded up to
+// whole blocks would leave 32 bits
+constexpr int kMostSize = 0x7fff0000;
+inline bool bad_size(int size) { return size < 0 || size > kMostSize; }
 inline bool short_ld(int ld, int rows) { return ld < (rows > 1 ? rows : 1); }
 
 }  // namespace xsymv

@@ -59,6 +59,7 @@ bool map_rows(CUtensorMap* map, CUtensorMapDataType type, int bytes, const void*
                 CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
+
 Prepare prepare_of(const int8_t* q, long long ldq, int rows, int k, long long width, void* out,
                    bool halves) {
   Prepare c{q, ldq, rows, k, width, out, halves, k % 16 == 0 && on_grid(q, ldq), 8};
@@ -211,9 +212,9 @@ int depth_split(long long tiles, int steps, long long slots) {
 
 int gemmq_entry(char type, int m, int n, int k, float alpha, const int8_t* W, int ldw, const float* sw,
                 const int8_t* X, int ldx, const float* sx, float beta, void* Y, int ldy) {
-  if (m < 0) return 1;
-  if (n < 0) return 2;
-  if (k < 0) return 3;
+  if (bad_size(m)) return 1;
+  if (bad_size(n)) return 2;
+  if (bad_size(k)) return 3;
   if (short_ld(ldw, k)) return 6;
   if (short_ld(ldx, k)) return 9;
   if (short_ld(ldy, m)) return 13;
@@ -224,13 +225,13 @@ int gemmq_entry(char type, int m, int n, int k, float alpha, const int8_t* W, in
   int dev, sms;
   if (!current_device(&dev, &sms)) return XSYMV_ERR_DEVICE;
   cudaStream_t st = current_stream();
-  const GemmqArgs a{m, n, k, alpha, W, ldw, sw, X, ldx, sx, beta, Y, ldy, type};
   if (no_product) {
     const GemmqArgs a{m, n, 0, 0.f, nullptr, 0, nullptr, nullptr, 0, nullptr, beta, Y, ldy, type};
     return launched(launch_after(scale_kernel, dim3((m + 255) / 256, std::min(n, 65535)), 256, 0,
                                  st, a),
                     1, st);
   }
+  const GemmqArgs a{m, n, k, alpha, W, ldw, sw, X, ldx, sx, beta, Y, ldy, type};
   if (n <= kFewTokens && k <= kFewMostDepth) {
     const bool g = k % 16 == 0 && on_grid(W, ldw) && on_grid(X, ldx);
     // off the grid a block's rows lie 16 apart, and every alignment has its blocks

@@ -125,7 +125,7 @@ __device__ __forceinline__ uint4 load16(const int8_t* row, int first, int k) {
 // they all lie `skew` bytes beyond a boundary, so W is read in aligned pieces and
 // only X, from L1, is shifted to meet them: element p of the shifted depth is
 // element p - skew of X, zero outside it (32768 x 8193, one token: 106 us with W
-// shifted, 49 us so).
+// shifted, 48 us so).
 constexpr int kFewTokens = 8, kFewMostDepth = 1 << 22;
 constexpr int kMmaWarps = 8, kMmaRows = 32, kFewStep = kMmaWarps * 64;
 __device__ __forceinline__ void mma_16x8x16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,

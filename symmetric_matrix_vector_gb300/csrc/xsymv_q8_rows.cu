@@ -739,7 +739,7 @@ int most_head(const T* p, long long ld) {
 // a thread of each operand: small blocks, of which many fit on an SM, so that
 // some load while others reduce.  Else as few as possible: one column's latency.
 // Columns that a warp holds go four to a block: blocks of one warp start too
-// slowly (16384 columns of 1024 halves: 17 us against 7).
+// slowly (quant, 16384 columns of 1024: 17.4 us against 8.9).
 struct Shape {
   int packs, threads;
   int columns(int n) const { return threads == 32 ? std::min(n, 4) : 1; }
@@ -761,8 +761,8 @@ Shape shape_for(int m, int n, int head, int most) {
 
 template <class T>
 int quant_entry(int m, int n, const T* X, int ldx, int8_t* Q, int ldq, float* scale) {
-  if (m < 0) return 1;
-  if (n < 0) return 2;
+  if (bad_size(m)) return 1;
+  if (bad_size(n)) return 2;
   if (short_ld(ldx, m)) return 4;
   if (short_ld(ldq, m)) return 6;
   if (m == 0 || n == 0) return XSYMV_OK;
@@ -781,8 +781,8 @@ int quant_entry(int m, int n, const T* X, int ldx, int8_t* Q, int ldq, float* sc
 
 template <class T>
 int dequant_entry(int m, int n, const int8_t* Q, int ldq, const float* scale, T* X, int ldx) {
-  if (m < 0) return 1;
-  if (n < 0) return 2;
+  if (bad_size(m)) return 1;
+  if (bad_size(n)) return 2;
   if (short_ld(ldq, m)) return 4;
   if (short_ld(ldx, m)) return 7;
   if (m == 0 || n == 0) return XSYMV_OK;
@@ -805,8 +805,8 @@ int dequant_entry(int m, int n, const int8_t* Q, int ldq, const float* scale, T*
 template <class T>
 int rmsquant_entry(int m, int n, const T* X, int ldx, const T* R, int ldr, const T* G, float eps,
                    T* H, int ldh, int8_t* Q, int ldq, float* scale, float* rstd) {
-  if (m < 0) return 1;
-  if (n < 0) return 2;
+  if (bad_size(m)) return 1;
+  if (bad_size(n)) return 2;
   if (short_ld(ldx, m)) return 4;
   if (R != nullptr && short_ld(ldr, m)) return 6;
   if (!(eps >= 0.f)) return 8;
@@ -853,8 +853,8 @@ GradKernel<T> grad_kernel(int packs, bool g) {
 template <class T>
 int rmsgrad_entry(int m, int n, const T* dY, int lddy, const T* H, int ldh, const T* G,
                   const float* rstd, const T* dR, int lddr, T* dX, int lddx, float* dG) {
-  if (m < 0) return 1;
-  if (n < 0) return 2;
+  if (bad_size(m)) return 1;
+  if (bad_size(n)) return 2;
   if (short_ld(lddy, m)) return 4;
   if (short_ld(ldh, m)) return 6;
   if (dR != nullptr && short_ld(lddr, m)) return 10;

@@ -63,3 +63,25 @@ def test_example_runs(capsys):
         if "within" in line:
             # two roundings of at most half a 254th of the largest value to every product
             assert float(line.split("within ")[1].split()[0]) < 0.03
+
+
+@pytest.mark.parametrize("tokens", [1, 17, 200])
+def test_serving_step_in_a_graph(tokens):
+    """captured after a first run on the stream, replayed on other inputs"""
+    layer, normal, x, r = make(torch.bfloat16, 300, 520, tokens)
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(stream):
+        layer.forward(x, r)
+    stream.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=stream):
+        y, h = layer.forward(x, r)
+        y, h = layer.forward(y[:, :1] + x, h)
+    for _ in range(3):
+        x.copy_(normal(tokens, 520))
+        graph.replay()
+        torch.cuda.synchronize()
+        y1, h1 = layer.forward(x, r)
+        y1, h1 = layer.forward(y1[:, :1] + x, h1)
+        assert torch.equal(y, y1) and torch.equal(h, h1)

@@ -105,3 +105,17 @@ def test_kinds_and_tensors():
     a = torch.zeros(4)
     with pytest.raises(ValueError):
         xs.xquant_s(4, 1, a, 4, P, 4, P, stream=0)
+
+
+def test_sizes_beyond_the_largest():
+    """indexes rounded up to whole blocks stay in 32 bits"""
+    big = 0x7fff0001
+    assert xs.xquant_b(big, 2, P, big, P, big, P, stream=0) == 1
+    assert xs.xquant_b(4, big, P, 4, P, 4, P, stream=0) == 2
+    assert xs.xdequant_b(big, 2, P, big, P, P, big, stream=0) == 1
+    assert xs.xrmsquant_b(big, 2, P, big, None, 0, None, 0.0, None, 0, P, big, P, None,
+                          stream=0) == 1
+    assert xs.xrmsgrad_b(big, 2, P, big, P, big, None, P, None, 0, P, big, None, stream=0) == 1
+    assert xs.xgemmq_b(big, 2, 4, 1.0, P, 4, None, P, 4, None, 0.0, P, big, stream=0) == 1
+    assert xs.xgemmq_b(4, big, 4, 1.0, P, 4, None, P, 4, None, 0.0, P, 4, stream=0) == 2
+    assert xs.xgemmq_b(4, 2, big, 1.0, P, big, None, P, big, None, 0.0, P, 4, stream=0) == 3
