@@ -126,15 +126,21 @@ cudaError_t allow_smem(int smem) {
 
 // The operands of a tiled product as its tensor copies take them: W in 8 bits and X in
 // 8 bits or (`halves`) as halves of a depth that is a multiple of kStepDepth.
-// What is not on 16-byte boundaries is copied first, in one launch.
+// What is not on 16-byte boundaries is copied first, in one launch, but for W with GRID
+// false: it gets maps of every 16th row from the boundary before its first.
+template <bool GRID>
 struct Operands {
-  CUtensorMap w, x;
+  MapsW<GRID> w;
+  CUtensorMap x;
   int *status, epoch, steps, kernels;
 };
-int prepare_operands(const GemmqArgs& a, bool halves, int rows_x, cudaStream_t st, Operands* o) {
-  o->steps = (int)((a.k + (long long)kStepDepth - 1) / kStepDepth);
-  const long long kp = (long long)o->steps * kStepDepth, ldo = (a.k + 15LL) / 16 * 16;
-  const bool move_w = !on_grid(a.W, a.ldw), move_x = halves || !on_grid(a.X, a.ldx);
+template <bool GRID>
+int prepare_operands(const GemmqArgs& a, bool halves, int rows_x, cudaStream_t st,
+                     Operands<GRID>* o) {
+  const long long steps = (a.k + (GRID ? 0LL : 15LL) + kStepDepth - 1) / kStepDepth;
+  o->steps = (int)steps;
+  const long long kp = steps * kStepDepth, ldo = (a.k + 15LL) / 16 * 16;
+  const bool move_w = GRID && !on_grid(a.W, a.ldw), move_x = halves || !on_grid(a.X, a.ldx);
   Pieces pieces;
   const size_t at_w = move_w ? pieces.add((size_t)a.m * ldo) : 0;
   const size_t at_x = move_x ? pieces.add((size_t)a.n * (halves ? kp * 2 : ldo)) : 0;
@@ -153,8 +159,18 @@ int prepare_operands(const GemmqArgs& a, bool halves, int rows_x, cudaStream_t s
   if (move_x) px = prepare_of(a.X, a.ldx, a.n, a.k, halves ? kp : ldo, ws + at_x, halves);
   const void* w = move_w ? pw.out : a.W;
   const void* x = move_x ? px.out : a.X;
-  if (!map_rows(&o->w, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, w, a.k, a.m, move_w ? ldo : a.ldw, 128))
-    return XSYMV_ERR_CUDA;
+  constexpr int kMaps = GRID ? 1 : 16;
+  for (int r = 0; r < kMaps; ++r) {
+    if (r >= a.m) {   // no such rows: none of that tile's results are
+      o->w.map[r] = o->w.map[0];
+      continue;
+    }
+    const int8_t* row = static_cast<const int8_t*>(w) + r * a.ldw;
+    const int skew = GRID ? 0 : (int)(reinterpret_cast<uintptr_t>(row) % 16);
+    if (!map_rows(&o->w.map[r], CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, row - skew, a.k + skew,
+                  (a.m - r + kMaps - 1) / kMaps, kMaps * (move_w ? ldo : a.ldw), 128))
+      return XSYMV_ERR_CUDA;
+  }
   if (halves ? !map_rows(&o->x, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, x, kp, a.n, kp * 2, rows_x)
              : !map_rows(&o->x, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, x, a.k, a.n,
                          move_x ? ldo : a.ldx, rows_x))
@@ -170,16 +186,30 @@ int prepare_operands(const GemmqArgs& a, bool halves, int rows_x, cudaStream_t s
   return XSYMV_OK;
 }
 
-template <int BN, bool RAW>
-int gemmq_streamed(const GemmqArgs& a, int split, cudaStream_t st) {
+// tiles of 128 channels: side by side, or (GRID false) 16 apart
+template <bool GRID>
+long long channel_tiles(int m) {
+  return GRID ? (m + 127LL) / 128 : 16 * ((m + 16 * 128 - 1LL) / (16 * 128));
+}
+
+// CTAs that share a tile's depth: twice as many while they all fit on the SMs
+int depth_split(long long tiles, long long steps, long long slots) {
+  int split = 1;
+  while (split < 8 && split * 2 <= steps && tiles * split * 2 <= slots) split *= 2;
+  return split;
+}
+
+template <int BN, bool RAW, bool GRID = true>
+int gemmq_streamed(const GemmqArgs& a, int sms, cudaStream_t st) {
   using S = Stream<BN, RAW>;
-  Operands o;
+  Operands<GRID> o;
   const int r = prepare_operands(a, !RAW, BN, st, &o);
   if (r != XSYMV_OK) return r;
-  cudaError_t e = allow_smem<gemmq_stream<BN, RAW>>(S::kSmem);
-  const long long tiles_m = (a.m + 127LL) / 128, tiles_n = (a.n + BN - 1LL) / BN;
+  cudaError_t e = allow_smem<gemmq_stream<BN, RAW, GRID>>(S::kSmem);
+  const long long tiles_m = channel_tiles<GRID>(a.m), tiles_n = (a.n + BN - 1LL) / BN;
+  const int split = depth_split(tiles_m * tiles_n, o.steps, S::kTwice ? 2LL * sms : sms);
   if (e == cudaSuccess)
-    e = launch_cluster(gemmq_stream<BN, RAW>, (unsigned)(tiles_m * tiles_n * split), split,
+    e = launch_cluster(gemmq_stream<BN, RAW, GRID>, (unsigned)(tiles_m * tiles_n * split), split,
                        S::kThreads, S::kSmem, true, st, o.w, o.x, a, (int)tiles_n, o.steps, split,
                        o.status, o.epoch, wait_limit_ns(), test_extra_tx());
   return launched(e, o.kernels, st, o.status, o.epoch);
@@ -188,7 +218,7 @@ int gemmq_streamed(const GemmqArgs& a, int split, cudaStream_t st) {
 template <int TOKENS>
 int gemmq_paired(const GemmqArgs& a, int sms, cudaStream_t st) {
   using S = Pairs<TOKENS>;
-  Operands o;
+  Operands<true> o;
   const int r = prepare_operands(a, true, S::kTokens / 2, st, &o);
   if (r != XSYMV_OK) return r;
   cudaError_t e = allow_smem<gemmq_pairs<TOKENS>>(S::kSmem);
@@ -198,16 +228,9 @@ int gemmq_paired(const GemmqArgs& a, int sms, cudaStream_t st) {
   order.tiles = order.tiles_m * order.tiles_n;
   if (e == cudaSuccess)
     e = launch_cluster(gemmq_pairs<TOKENS>, (unsigned)(2 * std::min(order.tiles, sms / 2)), 2, S::kThreads,
-                       S::kSmem, false, st, o.w, o.x, a, order, o.steps, o.status, o.epoch,
+                       S::kSmem, false, st, o.w.map[0], o.x, a, order, o.steps, o.status, o.epoch,
                        wait_limit_ns(), test_extra_tx());
   return launched(e, o.kernels, st, o.status, o.epoch);
-}
-
-// CTAs that share a tile's depth: twice as many while they all fit on the SMs
-int depth_split(long long tiles, int steps, long long slots) {
-  int split = 1;
-  while (split < 8 && split * 2 <= steps && tiles * split * 2 <= slots) split *= 2;
-  return split;
 }
 
 int gemmq_entry(char type, int m, int n, int k, float alpha, const int8_t* W, int ldw, const float* sw,
@@ -243,25 +266,29 @@ int gemmq_entry(char type, int m, int n, int k, float alpha, const int8_t* W, in
                                    a, split),
                     1, st);
   }
-  const int steps = (int)((k + (long long)kStepDepth - 1) / kStepDepth);
-  const long long rows = (m + 127LL) / 128;   // tiles of 128 channels
   if (n <= 64) {
-    const int split = depth_split(rows, steps, 2LL * sms);
-    if (n <= 32) return gemmq_streamed<32, true>(a, split, st);
+    // W off the grid: in tiles of rows 16 apart where there are rows to fill them, else
+    // copied to the grid (20 tokens; 4096 x 4095: 12.3 against 18.3 us, 32768 x 8193: 62
+    // against 163, but 1024 x 1001: 8.0 against 7.2, 300 x 14001: 19.6 against 14.9)
+    const bool g = on_grid(W, ldw) || m < 16 * 128;
+    if (n <= 32)
+      return g ? gemmq_streamed<32, true>(a, sms, st) : gemmq_streamed<32, true, false>(a, sms, st);
+    if (!g) return gemmq_streamed<64, true, false>(a, sms, st);
     // X's halves made in the tile's CTAs or once beforehand (64 tokens; 4096 x 4096: 11.5
     // against 13.1 us, 32768 x 8192: 63 against 53)
-    if ((long long)m * k <= 1LL << 26) return gemmq_streamed<64, true>(a, split, st);
-    return gemmq_streamed<64, false>(a, split, st);
+    if ((long long)m * k <= 1LL << 26) return gemmq_streamed<64, true>(a, sms, st);
+    return gemmq_streamed<64, false>(a, sms, st);
   }
   // 128 x 128 a CTA, or 256 x 192 or 256 x 256 a pair, whichever ends first by the clocks
   // that a step, a tile and a call take (measured)
   const auto up = [](long long x, long long by) { return (x + by - 1) / by; };
+  const long long steps = up(k, kStepDepth), rows = up(m, 128);
   const long long small = rows * up(n, 128), pairs = sms / 2;
   const int split = depth_split(small, steps, sms);
   const long long clocks_128 = up(small * split, sms) * (up(steps, split) * 800 + 8000);
   const long long clocks_192 = up(up(rows, 2) * up(n, 192), pairs) * steps * 780 + 12000;
-  const long long clocks_256 = up(up(rows, 2) * up(n, 256), pairs) * (steps * 1040LL + 9000);
-  if (clocks_128 <= std::min(clocks_192, clocks_256)) return gemmq_streamed<128, false>(a, split, st);
+  const long long clocks_256 = up(up(rows, 2) * up(n, 256), pairs) * (steps * 1040 + 9000);
+  if (clocks_128 <= std::min(clocks_192, clocks_256)) return gemmq_streamed<128, false>(a, sms, st);
   if (clocks_192 <= clocks_256) return gemmq_paired<192>(a, sms, st);
   return gemmq_paired<256>(a, sms, st);
 }

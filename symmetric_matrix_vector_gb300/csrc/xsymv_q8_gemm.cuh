@@ -337,16 +337,17 @@ __device__ __forceinline__ void store_columns(const GemmqArgs& a, uint32_t tmem,
 }
 
 // A CTA's share of a tile, in shared memory: `split` sets of sums to be added, each
-// `width` tokens from j on of 128 channels from i on, as [token / 4][channel][token % 4]
+// `width` tokens from j on of 128 channels i, i + apart, .., as
+// [token / 4][channel][token % 4]
 struct TileResult {
   uint32_t at;
-  int split, width, i;
+  int split, width, i, apart;
   long long j;
   const float *channel, *token;   // their factors
   bool failed;
 };
 // ... added, scaled and stored by all warps, 4 tokens of 32 * P channels at a time (P = 2:
-// two 16-bit results a lane, in one 4-byte store)
+// two 16-bit results a lane, in one 4-byte store, of channels side by side)
 template <class T, int P>
 __device__ __forceinline__ void store_result(const GemmqArgs& a, const TileResult& t, int threads) {
   const int warps = threads / 32, lane = threadIdx.x % 32, across = 4 / P;
@@ -370,7 +371,7 @@ __device__ __forceinline__ void store_result(const GemmqArgs& a, const TileResul
 #pragma unroll
       for (int e = 0; e < 4; ++e) v[q][e] *= channel;
     }
-    const long long i = (long long)t.i + at;
+    const long long i = t.i + (long long)at * t.apart;
     T* y = static_cast<T*>(a.Y) + (t.j + c) * a.ldy + i;
     const bool both = i + P <= a.m;
 #pragma unroll
@@ -436,9 +437,34 @@ __device__ __forceinline__ void multiply_step(uint32_t acc, uint32_t w, uint32_t
                         one);
 }
 
-template <int BN, bool RAW>
+// 16 integers `skew` (1 .. 15) places further up: 8 lanes in turn hold 128 of a row, the
+// first of them the 16 before (and those of this call for the next)
+__device__ __forceinline__ uint4 shifted_up(const uint4& q, uint4& before, unsigned skew) {
+  const int lane = threadIdx.x % 32, from = lane % 8 == 0 ? lane + 7 : lane - 1;
+  const uint4 got = make_uint4(
+      __shfl_sync(0xffffffffu, q.x, from), __shfl_sync(0xffffffffu, q.y, from),
+      __shfl_sync(0xffffffffu, q.z, from), __shfl_sync(0xffffffffu, q.w, from));
+  const uint4 l = lane % 8 == 0 ? before : got;
+  before = got;
+  uint32_t w[8] = {l.x, l.y, l.z, l.w, q.x, q.y, q.z, q.w};
+  const unsigned off = 16 - skew, bits = (off & 3) * 8;
+  shift_words<4>(w, off);
+  return make_uint4(__funnelshift_r(w[0], w[1], bits), __funnelshift_r(w[1], w[2], bits),
+                    __funnelshift_r(w[2], w[3], bits), __funnelshift_r(w[3], w[4], bits));
+}
+
+// Rows of W that start off the 16-byte grid (GRID false, with RAW): a tile has every 16th
+// row.  They all lie `skew` bytes beyond a boundary, so they have a tensor map of their own
+// that begins there, and X is shifted to meet them on its way to halves: element p of the
+// shifted depth is element p - skew of X, zero outside it.  (A copy of W on the grid first:
+// 32768 x 8193, 20 tokens, 163 us; so, 62.)
+template <bool GRID>
+struct MapsW {
+  CUtensorMap map[GRID ? 1 : 16];   // !GRID: rows r, r + 16, .. for each r
+};
+template <int BN, bool RAW, bool GRID>
 __global__ void __launch_bounds__(Stream<BN, RAW>::kThreads, Stream<BN, RAW>::kTwice ? 2 : 1)
-    gemmq_stream(const __grid_constant__ CUtensorMap map_w,
+    gemmq_stream(const __grid_constant__ MapsW<GRID> maps_w,
                  const __grid_constant__ CUtensorMap map_x, GemmqArgs a, int tiles_n, int steps,
                  int split, int* status, int epoch, unsigned long long limit_ns,
                  uint32_t extra_tx) {
@@ -461,7 +487,10 @@ __global__ void __launch_bounds__(Stream<BN, RAW>::kThreads, Stream<BN, RAW>::kT
   // tiles that share W side by side: it is read from HBM once
   const int tile = blockIdx.x / split, tm = tile / tiles_n, tn = tile - tm * tiles_n;
   // this CTA's channels and tokens, and its steps of the depth
-  const int row_w = tm * 128, row_x = tn * BN;
+  constexpr int kApart = GRID ? 1 : 16;
+  const int row_w = tm / kApart * 128, row_x = tn * BN;   // rows of the tensor maps
+  const int i0 = row_w * kApart + tm % kApart;            // channels i0, i0 + kApart, ..
+  const CUtensorMap* const map_w = &maps_w.map[tm % kApart];
   const int s0 = (int)((long long)steps * rank / split);
   const int mine = (int)((long long)steps * (rank + 1) / split) - s0;
 
@@ -469,7 +498,7 @@ __global__ void __launch_bounds__(Stream<BN, RAW>::kThreads, Stream<BN, RAW>::kT
   if (threadIdx.x == 0) {
     // the first steps of W on their way to L2 while the predecessor still runs
     for (int u = 0; u < min(mine, 8); ++u)
-      tensor_prefetch(&map_w, (s0 + u) * kStepDepth, row_w);
+      tensor_prefetch(map_w, (s0 + u) * kStepDepth, row_w);
     for (int s = 0; s < S::kStagesW; ++s) {
       mbar_init(w_full + 8 * s, 1);
       mbar_init(w_empty + 8 * s, 8);
@@ -508,7 +537,7 @@ __global__ void __launch_bounds__(Stream<BN, RAW>::kThreads, Stream<BN, RAW>::kT
       const uint32_t bar = full + 8 * stage;
       if (w) {
         mbar_arrive_expect_tx(bar, S::kBytesW + extra_tx);
-        tensor_g2s<1>(ring + stage * S::kBytesW, &map_w, depth, row_w, bar);
+        tensor_g2s<1>(ring + stage * S::kBytesW, map_w, depth, row_w, bar);
       } else if (RAW) {
         mbar_arrive_expect_tx(bar, S::kBytesRaw + extra_tx);
         tensor_g2s<1>(ring + S::kAtRaw + stage * S::kBytesRaw, &map_x, depth, row_x, bar);
@@ -578,6 +607,16 @@ __global__ void __launch_bounds__(Stream<BN, RAW>::kThreads, Stream<BN, RAW>::kT
   } else if (RAW && warp >= 12) {
     // ---- X to halves: 16 elements a thread in turn, 8 threads a token
     const int id = (int)threadIdx.x - 384;
+    const unsigned skew =
+        GRID ? 0 : (unsigned)(reinterpret_cast<uintptr_t>(a.W + min(i0, a.m - 1) * a.ldw) % 16);
+    uint4 before[GRID ? 1 : BN / 16];   // !GRID: the 16 elements before the step's, in id % 8 == 0
+    if (!GRID)
+#pragma unroll
+      for (int e = 0; e < BN / 16; ++e) {
+        const long long j = j0 + id / 8 + 16 * e;
+        before[e] = j < a.n && id % 8 == 0 ? load16<false>(a.X + j * a.ldx, s0 * kStepDepth - 16, a.k)
+                                           : make_uint4(0, 0, 0, 0);
+      }
     for (int u = 0; u < mine; ++u) {
       const int stage = u % COPIES, sa = u % S::kStagesA;
       ok = wait_or_dead(x_full + 8 * stage, u / COPIES & 1, dead, limit_ns);
@@ -591,6 +630,9 @@ __global__ void __launch_bounds__(Stream<BN, RAW>::kThreads, Stream<BN, RAW>::kT
         const int r = id / 8 + 16 * e, c = id % 8;
         q[e] = lds128(ring + S::kAtRaw + stage * S::kBytesRaw + r * 128 + ((c ^ (r & 7)) << 4));
       }
+      if (!GRID && skew != 0)
+#pragma unroll
+        for (int e = 0; e < BN / 16; ++e) q[e] = shifted_up(q[e], before[e], skew);
       ok = wait_or_dead(a_empty + 8 * sa, (u / S::kStagesA & 1) ^ 1, dead, limit_ns);
       if (!__all_sync(0xffffffffu, ok)) {
         ok = false;
@@ -621,8 +663,10 @@ __global__ void __launch_bounds__(Stream<BN, RAW>::kThreads, Stream<BN, RAW>::kT
     for (int c = lane; c < BN; c += 32)
       token_scale[c] = j0 + c < a.n ? token_factor(a, j0 + c) : 0.f;
 #pragma unroll 1
-    for (int c = lane; c < 128; c += 32)
-      channel_scale[c] = row_w + c < a.m && a.sw != nullptr ? a.sw[row_w + c] : 1.f;
+    for (int c = lane; c < 128; c += 32) {
+      const long long i = i0 + (long long)c * kApart;
+      channel_scale[c] = i < a.m && a.sw != nullptr ? a.sw[i] : 1.f;
+    }
   }
   // a warp's failure is the CTA's: its results are NaN
   __syncwarp();
@@ -632,7 +676,7 @@ __global__ void __launch_bounds__(Stream<BN, RAW>::kThreads, Stream<BN, RAW>::kT
     tensor_fence_after();
     if (warp >= 4 && warp < 12) {
       const int at = quarter * 32 + lane;
-      const long long i = (long long)row_w + at;
+      const long long i = i0 + (long long)at * kApart;
       const float channel = *dead != 0 ? __uint_as_float(0x7fc00000u) : channel_scale[at];
       const uint32_t from = tmem + ((uint32_t)(quarter * 32) << 16);
       if (a.type == 's')
@@ -669,11 +713,11 @@ __global__ void __launch_bounds__(Stream<BN, RAW>::kThreads, Stream<BN, RAW>::kT
     }
     cluster_sync();
     const long long j = j0 + rank * width;
-    const TileResult t{ring, split, width, row_w, j, channel_scale, token_scale + rank * width,
-                       *dead != 0};
+    const TileResult t{ring, split, width, i0, kApart, j, channel_scale,
+                       token_scale + rank * width, *dead != 0};
     if (a.type == 's')
       store_result<float, 1>(a, t, S::kThreads);
-    else if (((reinterpret_cast<uintptr_t>(a.Y) | (uintptr_t)a.ldy * 2) & 3) != 0)
+    else if (!GRID || ((reinterpret_cast<uintptr_t>(a.Y) | (uintptr_t)a.ldy * 2) & 3) != 0)
       a.type == 'h' ? store_result<__half, 1>(a, t, S::kThreads)
                     : store_result<__nv_bfloat16, 1>(a, t, S::kThreads);
     else

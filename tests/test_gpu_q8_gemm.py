@@ -326,3 +326,26 @@ def test_waits_that_run_out(m, n, k):
     # a call without such waits reports none
     s = torch.empty((1,), device="cuda")
     assert xs.quant("s", 4, 1, y, 4, w, 4, s) == 0 and xs.xsymv_sync_status() == 0
+
+
+@pytest.mark.parametrize("n", [9, 20, 32, 33, 47, 64])
+@pytest.mark.parametrize("m", [1, 15, 17, 300, 2047, 2049, 4100])
+def test_rows_off_the_16_byte_boundaries(n, m):
+    """W's rows at every distance from a boundary, X's at another one or on it, the largest
+    integers all around both; exact sums"""
+    g = gen(m + n)
+    for k, pad, off, pad_x, off_x in ((1, 0, 3, 0, 0), (15, 2, 0, 1, 0), (113, 0, 0, 15, 16),
+                                      (128, 1, 15, 0, 0), (129, 15, 1, 15, 0), (127, 1, 1, 2, 9),
+                                      (1000, 4, 2, 8, 0), (640, 8, 8, 0, 7)):
+        def placed(rows, pad, off):
+            flat = torch.full((off + rows * (k + pad) + 300,), 127, dtype=torch.int8, device="cuda")
+            at = flat[off:off + rows * (k + pad)].view(rows, k + pad)
+            at[:, :k] = integers(g, rows, k, -128, 127)
+            return flat, at
+        (wf, w), (xf, x) = placed(m, pad, off), placed(n, pad_x, off_x)
+        y = torch.full((n + 1, m + 3), 7.0, device="cuda")
+        assert xs.gemmq("s", m, n, k, 1.0, wf.data_ptr() + off, k + pad, None, xf.data_ptr() + off_x,
+                        k + pad_x, None, 0.0, y, m + 3) == 0
+        torch.cuda.synchronize()
+        assert torch.equal(y[:n, :m].double(), x[:, :k].double() @ w[:, :k].double().T), (k, pad, off)
+        assert bool((y[n:] == 7.0).all()) and bool((y[:, m:] == 7.0).all())
