@@ -304,7 +304,7 @@ struct Stream {
   static constexpr int kRing = kAtRaw + kStagesRaw * kBytesRaw;
   static constexpr int kSmem = kRing + 1024;
   static_assert(BN + kStagesA * kColumnsA <= kColumns, "tensor memory");
-  static_assert(BN * 128 * 4 <= kRing, "the exchange of sums");
+  static_assert((BN + 31) / 32 * 32 * 128 * 4 <= kRing, "the exchange of sums");
 };
 
 // A whole depth's sums, straight from tensor memory: this warp's 32 channels, 16 tokens of
@@ -336,12 +336,12 @@ __device__ __forceinline__ void store_columns(const GemmqArgs& a, uint32_t tmem,
   }
 }
 
-// A CTA's share of a tile, in shared memory: `split` sets of sums to be added, each
-// `width` tokens from j on of 128 channels i, i + apart, .., as
+// A CTA's share of a tile, in shared memory: `split` sets of sums to be added, `width` tokens
+// apart, each `share` (if positive) tokens from j on of 128 channels i, i + apart, .., as
 // [token / 4][channel][token % 4]
 struct TileResult {
   uint32_t at;
-  int split, width, i, apart;
+  int split, width, share, i, apart;
   long long j;
   const float *channel, *token;   // their factors
   bool failed;
@@ -352,7 +352,7 @@ template <class T, int P>
 __device__ __forceinline__ void store_result(const GemmqArgs& a, const TileResult& t, int threads) {
   const int warps = threads / 32, lane = threadIdx.x % 32, across = 4 / P;
 #pragma unroll 1
-  for (int u = threadIdx.x / 32; u < t.width / 4 * across; u += warps) {
+  for (int u = threadIdx.x / 32; u < t.share / 4 * across; u += warps) {
     const int c = u / across * 4, at = (u % across * 32 + lane) * P;
     float v[P][4];
 #pragma unroll
@@ -693,7 +693,7 @@ __global__ void __launch_bounds__(Stream<BN, RAW>::kThreads, Stream<BN, RAW>::kT
     // that every CTA has finished with
     cluster_sync();
     tensor_fence_after();
-    const int width = BN / split;
+    const int width = (BN / split + 3) / 4 * 4;
     if (warp >= 4 && warp < 12) {
       const bool good = *dead == 0;
 #pragma unroll 1
@@ -713,7 +713,8 @@ __global__ void __launch_bounds__(Stream<BN, RAW>::kThreads, Stream<BN, RAW>::kT
     }
     cluster_sync();
     const long long j = j0 + rank * width;
-    const TileResult t{ring, split, width, i0, kApart, j, channel_scale,
+    const int share = min(width, BN - rank * width);   // 48 tokens in 8 shares: none of the last two
+    const TileResult t{ring, split, width, share, i0, kApart, j, channel_scale,
                        token_scale + rank * width, *dead != 0};
     if (a.type == 's')
       store_result<float, 1>(a, t, S::kThreads);
