@@ -29,7 +29,7 @@ using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, 
                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
-// the driver's tensor map encoder (the library does not link the driver)
+// the CUDA driver's tensor map encoder (the library does not link libcuda)
 EncodeTiled encoder() {
   static const EncodeTiled fn = [] {
     void* p = nullptr;

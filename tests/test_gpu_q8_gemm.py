@@ -349,3 +349,20 @@ def test_rows_off_the_16_byte_boundaries(n, m):
         torch.cuda.synchronize()
         assert torch.equal(y[:n, :m].double(), x[:, :k].double() @ w[:, :k].double().T), (k, pad, off)
         assert bool((y[n:] == 7.0).all()) and bool((y[:, m:] == 7.0).all())
+
+
+@pytest.mark.parametrize("m,n,k", [(2500, 20, 641), (2500, 40, 641), (4100, 64, 333), (700, 40, 640),
+                                   (300, 48, 4096)])
+def test_waits_that_run_out_off_the_boundaries(m, n, k):
+    """the same for W's rows off the 16-byte boundaries, and for tiles of 48 tokens"""
+    test_waits_that_run_out(m, n, k)
+
+
+@pytest.mark.parametrize("n", [33, 40, 47, 48])
+def test_tiles_of_48_tokens(n):
+    """their depth shared by 1, 2, 4 and 8 CTAs"""
+    g = gen(n)
+    for kind, m, k, pad in (("b", 40000, 64, 0), ("h", 20000, 256, 16), ("s", 6000, 512, 0),
+                            ("h", 257, 2000, 3), ("b", 128, 1024, 0), ("s", 129, 4097, 0)):
+        check(kind, m, n, k, g, pad)
+        check(kind, m, n, k, g, pad, 1, -0.5, 2.0)
