@@ -16,6 +16,7 @@
 // Multiply-adds are written out, so that a call with an optional operand left
 // out rounds as the same call with that operand given.
 #include <algorithm>
+#include <type_traits>
 
 #include "xsymv_q8.cuh"
 
@@ -25,56 +26,6 @@ namespace {
 constexpr int kWarps = 32;   // of a block, at most
 constexpr int kSmemPerSm = 227 * 1024;
 constexpr int kBlockSmem = 2048;   // a block's reserve and its reduction buffers
-
-// ---------------------------------------------------------- a warp's store --
-
-// store8 of a warp's 32 packs in a row, all lanes at once.  Off the 16-byte
-// grid every lane writes the aligned pieces that begin in the previous
-// lane's pack; the warp's first and last pieces, shared with other warps, are
-// written element by element.
-template <bool GRID, class T>
-__device__ __forceinline__ void store_warp(T* row, int first, int m, const Raw<T>& r) {
-  constexpr int N = Raw<T>::N;
-  if (GRID) {
-    store8<true>(row, first, m, r);
-    return;
-  }
-  const uintptr_t at = reinterpret_cast<uintptr_t>(row) + (long long)first * (int)sizeof(T);
-  const unsigned off = at % 16;
-  if (off == 0 || !__all_sync(0xffffffffu, first + kPack <= m)) {
-    store8<false>(row, first, m, r);
-    return;
-  }
-  // this lane's pieces are the N words from byte 16 - off of
-  // (the previous lane's last 16 bytes, this lane's pack)
-  uint32_t w[N + 4];
-#pragma unroll
-  for (int k = 0; k < 4; ++k) w[k] = __shfl_up_sync(0xffffffffu, r.w[N - 4 + k], 1);
-#pragma unroll
-  for (int k = 0; k < N; ++k) w[4 + k] = r.w[k];
-  const unsigned skip = 16 - off;
-  shift_words<N>(w, skip);
-#pragma unroll
-  for (int k = 0; k < N; ++k)
-    w[k] = sizeof(T) == 4 ? w[k] : __funnelshift_r(w[k], w[k + 1], (skip & 3) * 8);
-  const int lane = threadIdx.x % 32, own = (int)(skip / sizeof(T));   // elements before a piece ends
-#pragma unroll
-  for (int k = 0; k < N; k += 4)
-    if (k > 0 || lane > 0)
-      *reinterpret_cast<uint4*>(at - off + 4 * k) = make_uint4(w[k], w[k + 1], w[k + 2], w[k + 3]);
-  if (lane == 0) store8<false>(row + first, 0, own, r);
-  if (lane == 31) {
-#pragma unroll
-    for (int e = 0; e < kPack; ++e)
-      if (e * (int)sizeof(T) >= kPack * (int)sizeof(T) - (int)off) {
-        const uint32_t b = r.w[e * sizeof(T) / 4] >> (e * sizeof(T) % 4 * 8);
-        if (sizeof(T) == 4)
-          *reinterpret_cast<uint32_t*>(row + first + e) = b;
-        else
-          *reinterpret_cast<uint16_t*>(row + first + e) = (uint16_t)b;
-      }
-  }
-}
 
 // the larger magnitude of |top|, |v.x| and |v.y|; a NaN wins
 __device__ __forceinline__ float larger(float top, float2 v) {
@@ -428,54 +379,50 @@ struct RmsgradArgs {
   float* parts;      // gridDim.x partial sums of dG, m apart; NULL: none wanted
 };
 
-// A pack's aligned pieces copied to shared memory without a stop at a
-// register, and its elements from there.  `slot`: the first of the pack's
-// PIECES 16-byte pieces of this thread, `apart` bytes from the next.  Off the
-// grid a pack has one piece more.  Packs at a column's end are loaded element by
-// element and kept as if on the grid; packs beyond it are never fetched.
-template <class T, bool GRID>
+// How the operands of a gradient lie: every column of whole packs on the 16-byte grid; all on
+// the grid that dX's columns lie on; or each on its own
+enum Lie { kOnGrid, kAlike, kAnyhow };
+
+// A pack's aligned pieces copied to shared memory without a stop at a register, and its
+// elements from there.  `slot`: the first of the pack's PIECES 16-byte pieces of this thread,
+// `apart` bytes from the next.  kAnyhow: a pack has one piece more.  Pieces without an element
+// of the column are never fetched; elements outside it are made zero on the way out.
+template <class T, Lie LIE>
 struct Slot {
-  static constexpr int N = Raw<T>::N, PIECES = N / 4 + (GRID ? 0 : 1);
-  static __device__ __forceinline__ void put(uint32_t at, uint32_t a, uint32_t b, uint32_t c,
-                                             uint32_t d) {
-    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(a), "r"(b), "r"(c),
-                 "r"(d)
-                 : "memory");
-  }
+  static constexpr int N = Raw<T>::N, PIECES = N / 4 + (LIE == kAnyhow ? 1 : 0);
   static __device__ __forceinline__ void clear(uint32_t slot, uint32_t apart) {
 #pragma unroll
-    for (int k = 0; k < PIECES; ++k) put(slot + k * apart, 0, 0, 0, 0);
+    for (int k = 0; k < PIECES; ++k)
+      asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(slot + k * apart), "r"(0)
+                   : "memory");
   }
-  static __device__ __forceinline__ unsigned off(const T* row, int first, int m) {
-    return GRID || first + kPack > m
-               ? 0
-               : (unsigned)(reinterpret_cast<uintptr_t>(row + first) % 16);
+  static __device__ __forceinline__ bool whole(int first, int m) {
+    return LIE == kOnGrid || (first >= 0 && first + kPack <= m);
+  }
+  static __device__ __forceinline__ unsigned off(const T* row, int first) {
+    return LIE != kAnyhow ? 0 : (unsigned)(reinterpret_cast<uintptr_t>(row + first) % 16);
   }
   static __device__ __forceinline__ void fetch(uint32_t slot, uint32_t apart, const T* row,
                                                int first, int m) {
     if (first >= m) return;
-    if (GRID || first + kPack <= m) {
-      const unsigned o = off(row, first, m);
-      const char* at = reinterpret_cast<const char*>(row + first) - o;
+    constexpr int E = 16 / (int)sizeof(T);
+    const unsigned o = off(row, first);
+    const char* at = reinterpret_cast<const char*>(row + first) - o;
+    const int e = first - (int)(o / sizeof(T));
 #pragma unroll
-      for (int k = 0; k < PIECES; ++k)
-        if (k < N / 4 || o != 0) {
-          // where two requests share every 32-byte sector they meet in L1
-          if (GRID && PIECES == 1)
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(slot + k * apart),
-                         "l"(at + 16 * k)
-                         : "memory");
-          else
-            asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(slot + k * apart),
-                         "l"(at + 16 * k)
-                         : "memory");
-        }
-    } else {
-      const Raw<T> r = load8<false>(row, first, m);
-#pragma unroll
-      for (int k = 0; k < N; k += 4)
-        put(slot + k / 4 * apart, r.w[k], r.w[k + 1], r.w[k + 2], r.w[k + 3]);
-    }
+    for (int k = 0; k < PIECES; ++k)
+      if ((k < N / 4 || o != 0) &&
+          (whole(first, m) || (e + (k + 1) * E > 0 && e + k * E < m))) {
+        // where two requests share every 32-byte sector they meet in L1
+        if (PIECES == 1)
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(slot + k * apart),
+                       "l"(at + 16 * k)
+                       : "memory");
+        else
+          asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(slot + k * apart),
+                       "l"(at + 16 * k)
+                       : "memory");
+      }
   }
   static __device__ __forceinline__ Raw<T> get(uint32_t slot, uint32_t apart, const T* row,
                                                int first, int m) {
@@ -487,35 +434,45 @@ struct Slot {
                    : "=r"(w[4 * k]), "=r"(w[4 * k + 1]), "=r"(w[4 * k + 2]), "=r"(w[4 * k + 3])
                    : "r"(slot + k * apart)
                    : "memory");
-    const unsigned o = off(row, first, m);
-    if (!GRID) shift_words<N>(w, o);
+    const unsigned o = off(row, first);
+    if (LIE == kAnyhow) shift_words<N>(w, o);
 #pragma unroll
     for (int k = 0; k < N; ++k)
-      r.w[k] = GRID || sizeof(T) == 4 ? w[k] : __funnelshift_r(w[k], w[k + 1], (o & 3) * 8);
+      r.w[k] = LIE != kAnyhow || sizeof(T) == 4 ? w[k]
+                                                : __funnelshift_r(w[k], w[k + 1], (o & 3) * 8);
+    if (!whole(first, m))
+#pragma unroll
+      for (int e = 0; e < kPack; ++e)
+        if (first + e < 0 || first + e >= m)
+          r.w[e * sizeof(T) / 4] &= sizeof(T) == 4 ? 0u : e % 2 == 0 ? 0xffff0000u : 0xffffu;
     return r;
   }
 };
 
 // A block takes columns j = block, block + gridDim.x, ... and sums its
 // share of dG in registers on the way; the shares are added by
-// weight_sum_kernel, in block order.  KNV packs a thread.  An element's place
-// has to be the same in every column, so the packs begin at element 0 whatever
-// the alignment.  The operands of the next stages - 1 columns are on their
+// weight_sum_kernel, in block order.  KNV packs a thread, on dX's grid.  An element's place
+// has to be the same in all of a block's columns, so gridDim.x is a multiple of kSameGrid
+// where a block has more than one: columns that far apart lie alike whatever the leading
+// dimension (packs from element 0 on, every column shifted into place: 4099 x 8192 halves
+// 98 us; so, 67).  The operands of the next stages - 1 columns are on their
 // way to shared memory meanwhile, every thread's packs to slots of its own
 // (no thread waits for another's copies).
+constexpr int kSameGrid = 8;   // 16 bytes / 2
 constexpr int kMostStages = 3;
 constexpr int kGradOperands = 3;
 // 16-byte pieces of shared memory a thread and stage
-template <class T, int KNV, bool GRID>
-constexpr int kGradSlots = kGradOperands * KNV * Slot<T, GRID>::PIECES;
+template <class T, int KNV, Lie LIE>
+constexpr int kGradSlots = kGradOperands * KNV * Slot<T, LIE>::PIECES;
 
-template <class T, int KNV, bool GRID>
-__global__ void __launch_bounds__(512, GRID && KNV <= 2 ? 2 : 1)
+template <class T, int KNV, Lie LIE>
+__global__ void __launch_bounds__(512, LIE != kAnyhow && KNV <= 2 ? 2 : 1)
     rmsgrad_kernel(RmsgradArgs<T> a, int stages) {
-  using S = Slot<T, GRID>;
+  using S = Slot<T, LIE>;
   extern __shared__ uint4 slots[];
   __shared__ float2 buf[2][kWarps];
   await_predecessor();
+  const int head = head_of<LIE == kOnGrid>(a.dX + (long long)blockIdx.x * a.lddx);
   const uint32_t apart = blockDim.x * 16u;
   const uint32_t mine = (uint32_t)__cvta_generic_to_shared(slots) + threadIdx.x * 16u;
   auto slot = [&](int stage, int operand, int p) {
@@ -528,7 +485,7 @@ __global__ void __launch_bounds__(512, GRID && KNV <= 2 ? 2 : 1)
       const T* dr = a.dR + j * a.lddr;
 #pragma unroll
       for (int p = 0; p < KNV; ++p) {
-        const int first = first_of(p, 0);
+        const int first = first_of(p, head);
         S::fetch(slot(stage, 0, p), apart, dy, first, a.m);
         S::fetch(slot(stage, 1, p), apart, h, first, a.m);
         if (a.dR != nullptr) S::fetch(slot(stage, 2, p), apart, dr, first, a.m);
@@ -542,7 +499,7 @@ __global__ void __launch_bounds__(512, GRID && KNV <= 2 ? 2 : 1)
     for (int o = 0; o < kGradOperands; ++o)
 #pragma unroll
       for (int p = 0; p < KNV; ++p)
-        if (first_of(p, 0) >= a.m || (o == 2 && a.dR == nullptr)) S::clear(slot(s, o, p), apart);
+        if (first_of(p, head) >= a.m || (o == 2 && a.dR == nullptr)) S::clear(slot(s, o, p), apart);
   Raw<T> g[KNV];
   float2 dg[KNV][kPack / 2];
 #pragma unroll
@@ -550,7 +507,7 @@ __global__ void __launch_bounds__(512, GRID && KNV <= 2 ? 2 : 1)
     Floats one;
 #pragma unroll
     for (int k = 0; k < kPack / 2; ++k) one.v[k] = make_float2(1.f, 1.f);
-    g[p] = a.G != nullptr ? load8<GRID>(a.G, first_of(p, 0), a.m) : raw_of<T>(one);
+    g[p] = a.G != nullptr ? load8<LIE == kOnGrid>(a.G, first_of(p, head), a.m) : raw_of<T>(one);
 #pragma unroll
     for (int k = 0; k < kPack / 2; ++k) dg[p][k] = make_float2(0.f, 0.f);
   }
@@ -575,7 +532,7 @@ __global__ void __launch_bounds__(512, GRID && KNV <= 2 ? 2 : 1)
     float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
     for (int p = 0; p < KNV; ++p) {
-      const int first = first_of(p, 0);
+      const int first = first_of(p, head);
       const Floats d = floats_of(S::get(slot(stage, 0, p), apart, dy, first, a.m));
       const Floats u = floats_of(S::get(slot(stage, 1, p), apart, h, first, a.m));
       const Floats w = floats_of(g[p]);
@@ -589,7 +546,7 @@ __global__ void __launch_bounds__(512, GRID && KNV <= 2 ? 2 : 1)
     const float c = -block_sum_max(SumMax{sum.x + sum.y, 0.f}, buf[phase]).sum / (float)a.m;
 #pragma unroll
     for (int p = 0; p < KNV; ++p) {
-      const int first = first_of(p, 0);
+      const int first = first_of(p, head);
       Floats d = floats_of(S::get(slot(stage, 0, p), apart, dy, first, a.m));
       const Floats u = floats_of(S::get(slot(stage, 1, p), apart, h, first, a.m));
       const Floats r = floats_of(
@@ -601,7 +558,7 @@ __global__ void __launch_bounds__(512, GRID && KNV <= 2 ? 2 : 1)
                             __ffma2_rn(__fmul2_rn(u.v[k], rstd2), make_float2(c, c),
                                        __fmul2_rn(d.v[k], w.v[k])),
                             r.v[k]);
-      store_warp<GRID>(a.dX + j * a.lddx, first, a.m, raw_of<T>(d));
+      store8<LIE == kOnGrid>(a.dX + j * a.lddx, first, a.m, raw_of<T>(d));
     }
     stage = stage + 1 == stages ? 0 : stage + 1;
   }
@@ -610,9 +567,9 @@ __global__ void __launch_bounds__(512, GRID && KNV <= 2 ? 2 : 1)
     for (int p = 0; p < KNV; ++p)
 #pragma unroll
       for (int k = 0; k < kPack / 2; ++k) {
-        const int i = first_of(p, 0) + 2 * k;
-        if (i < a.m) a.parts[(long long)blockIdx.x * a.m + i] = dg[p][k].x;
-        if (i + 1 < a.m) a.parts[(long long)blockIdx.x * a.m + i + 1] = dg[p][k].y;
+        const int i = first_of(p, head) + 2 * k;
+        if (i >= 0 && i < a.m) a.parts[(long long)blockIdx.x * a.m + i] = dg[p][k].x;
+        if (i >= -1 && i + 1 < a.m) a.parts[(long long)blockIdx.x * a.m + i + 1] = dg[p][k].y;
       }
   }
 }
@@ -875,18 +832,16 @@ struct GradKernel {
   int slots;
 };
 template <class T>
-GradKernel<T> grad_kernel(int packs, bool g) {
-  switch (packs) {
-    case 1:
-      return g ? GradKernel<T>{rmsgrad_kernel<T, 1, true>, kGradSlots<T, 1, true>}
-               : GradKernel<T>{rmsgrad_kernel<T, 1, false>, kGradSlots<T, 1, false>};
-    case 2:
-      return g ? GradKernel<T>{rmsgrad_kernel<T, 2, true>, kGradSlots<T, 2, true>}
-               : GradKernel<T>{rmsgrad_kernel<T, 2, false>, kGradSlots<T, 2, false>};
-    default:
-      return g ? GradKernel<T>{rmsgrad_kernel<T, 4, true>, kGradSlots<T, 4, true>}
-               : GradKernel<T>{rmsgrad_kernel<T, 4, false>, kGradSlots<T, 4, false>};
-  }
+GradKernel<T> grad_kernel(int packs, Lie lie) {
+  auto of = [&](auto knv) {
+    constexpr int K = decltype(knv)::value;
+    return lie == kOnGrid  ? GradKernel<T>{rmsgrad_kernel<T, K, kOnGrid>, kGradSlots<T, K, kOnGrid>}
+           : lie == kAlike ? GradKernel<T>{rmsgrad_kernel<T, K, kAlike>, kGradSlots<T, K, kAlike>}
+                           : GradKernel<T>{rmsgrad_kernel<T, K, kAnyhow>, kGradSlots<T, K, kAnyhow>};
+  };
+  return packs == 1   ? of(std::integral_constant<int, 1>())
+         : packs == 2 ? of(std::integral_constant<int, 2>())
+                      : of(std::integral_constant<int, 4>());
 }
 
 template <class T>
@@ -907,28 +862,37 @@ int rmsgrad_entry(int m, int n, const T* dY, int lddy, const T* H, int ldh, cons
   const bool g = m % kPack == 0 && most_head(dY, lddy) == 0 && most_head(H, ldh) == 0 &&
                  most_head(G, 0) == 0 && (dR == nullptr || most_head(dR, lddr) == 0) &&
                  most_head(dX, lddx) == 0;
-  // On the grid few packs a thread, so that two blocks of 512 threads fit on an SM
-  // (4096 x 16384 halves: 1 pack 86 us, 4 packs in blocks of 128 threads 90); off it, where
-  // a pack takes twice the registers, small blocks (4099 x 8192: 104 us against 146)
-  Shape s = shape_for<T>(m, g ? 1 : n, 0, 512);
-  const GradKernel<T> kernel = grad_kernel<T>(s.packs, g);
+  // Whether every operand's columns lie on their 16-byte grids as dX's do.  (Not asked where a
+  // block has one column: kAnyhow, with twice the registers, is sooner through it: 1543 x 257
+  // halves 7.8 us against 9.2.)
+  const auto as_dx = [&](const T* p, int ld) {
+    return (reinterpret_cast<uintptr_t>(p) - reinterpret_cast<uintptr_t>(dX)) % 16 == 0 &&
+           ((long long)ld - lddx) * (long long)sizeof(T) % 16 == 0;
+  };
+  const bool alike = n > 2 * sms && as_dx(dY, lddy) && as_dx(H, ldh) && (dR == nullptr || as_dx(dR, lddr));
+  // There few packs a thread, so that two blocks of 512 threads fit on an SM
+  // (4096 x 16384 halves: 1 pack 86 us, 4 packs in blocks of 128 threads 90); elsewhere, where
+  // a pack takes twice the registers, small blocks
+  Shape s = shape_for<T>(m, alike ? 1 : n, most_head(dX, lddx), 512);
+  const GradKernel<T> kernel = grad_kernel<T>(s.packs, g ? kOnGrid : alike ? kAlike : kAnyhow);
   const long long stage_bytes = (long long)kernel.slots * 16 * s.threads;
   if (stage_bytes > kSmemPerSm - kBlockSmem) s.packs = 0;
   // Blocks that share the columns: as many as an SM holds (or of the long columns'
   // dG shares of at least 64 columns), each with the stages that its share of
-  // the memory allows, on the grid two at least
-  int per_sm = std::max(1, (g && s.packs <= 2 ? 1024 : 512) / s.threads);
+  // the memory allows, two at least where all lie alike
+  int per_sm = std::max(1, (alike && s.packs <= 2 ? 1024 : 512) / s.threads);
   // ... but of more than 512 threads an SM only as many as take 4 columns each: every block has
   // partial sums of dG to write (4096 x 500 halves: 11.6 against 13.8 us, 1024 x 2000 floats:
   // 16.0 against 18.2)
   per_sm = (int)std::min<long long>(per_sm,
                                     std::max((511 + s.threads) / s.threads, n / (4 * sms)));
-  while (g && per_sm > 1 && kSmemPerSm / per_sm - kBlockSmem < 2 * stage_bytes) --per_sm;
+  while (alike && per_sm > 1 && kSmemPerSm / per_sm - kBlockSmem < 2 * stage_bytes) --per_sm;
   while (per_sm > 1 && kSmemPerSm / per_sm - kBlockSmem < stage_bytes) --per_sm;
   const int stages = (int)std::min<long long>(
       kMostStages, std::max<long long>(1, (kSmemPerSm / per_sm - kBlockSmem) / stage_bytes));
   const size_t smem = (size_t)(stages * stage_bytes);
-  const int blocks = s.packs > 0 ? (int)std::min<long long>(n, (long long)sms * per_sm)
+  const int most_blocks = sms * per_sm / kSameGrid * kSameGrid;
+  const int blocks = s.packs > 0 ? std::min(n, most_blocks)
                                  : (int)std::min<long long>((n + 63LL) / 64, 65535);
   float* parts = nullptr;
   if (dG != nullptr && n > 0) {

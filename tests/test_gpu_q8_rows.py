@@ -399,3 +399,39 @@ def test_rows_offsets_beyond_32_bits():
     assert torch.equal(rows, (q.float() * s[:, None]).bfloat16())
     del flat, qf, rows, q
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("kind", ["s", "h", "b"])
+@pytest.mark.parametrize("m,n", [(3, 6000), (61, 6000), (515, 3001), (1543, 1500), (4101, 700)])
+def test_rmsgrad_of_many_columns_at_every_alignment(kind, m, n):
+    """several columns a block; operands that lie alike and that do not; NaN all around"""
+    g = gen(m * n)
+    dt = DTYPES[kind]
+    nan = float("nan")
+
+    class Placed:
+        def __init__(self, pad, off, values):
+            self.flat = torch.full((off + n * (m + pad) + 9,), nan, dtype=dt, device="cuda")
+            self.rows = self.flat.as_strided((n, m), (m + pad, 1), off)
+            self.rows.copy_(values)
+            self.ptr, self.ld = self.flat.data_ptr() + off * self.flat.element_size(), m + pad
+
+    dy0, dr0 = normal(g, n, m, kind, 0.1), normal(g, n, m, kind, 0.1)
+    h0 = normal(g, n, m, kind, 2.0)
+    w = (1 + 0.2 * torch.randn((m,), generator=g, device="cuda")).to(dt)
+    rstd = torch.rsqrt(h0.float().square().mean(1) + EPS)
+    dx64, dg64, dx_size, dg_size = ref.rmsgrad(dy0.double(), h0.double(), w.double(), rstd.double(),
+                                               dr0.double())
+    bound = UNIT[kind] * dx64.abs() + (1 + UNIT[kind]) * ref.sum_depth(m) * U32 * dx_size
+    if kind == "h":
+        bound = bound + 2.0 ** -25
+    for at in (((0, 0),) * 4, ((1, 3),) * 4, ((8, 5),) * 4, ((0, 1), (3, 0), (2, 7), (1, 0)),
+               ((0, 2), (0, 2), (0, 2), (0, 0)), ((0, 0), (8, 8), (16, 0), (0, 16))):
+        dy, h, dr, dx = (Placed(*p, v) for p, v in zip(at, (dy0, h0, dr0, torch.zeros_like(h0))))
+        dg = torch.full((m,), -1.0, device="cuda")
+        assert run_rmsgrad(kind, m, n, dy, h, w, rstd, dr, dx, dg) == 0
+        torch.cuda.synchronize()
+        assert bool(((dx.rows.double() - dx64).abs() <= bound).all()), at
+        assert bool(((dg.double() - dg64).abs() <= (n + 40) * U32 * dg_size).all()), at
+        dx.rows.fill_(nan)
+        assert bool(torch.isnan(dx.flat).all()), at
